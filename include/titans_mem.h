@@ -37,6 +37,8 @@
 #ifndef TITANS_MEM_H
 #define TITANS_MEM_H
 
+#include <stddef.h>
+
 #ifdef __cplusplus
 extern "C" {
 #endif
@@ -311,6 +313,135 @@ int titans_mem_version(void);
  * tanh.approx. All three arrays are caller-owned device memory of n floats, asynchronous on
  * `stream`. TITANS_EINVAL for n < 0 or a NULL pointer, TITANS_ECUDA for a failed launch. */
 titans_status_t titans_silu_routes(const float *h, float *silu_fma, float *silu_mufu, long n, void *stream);
+
+/* ------------------------------------------------------------------ gated delta rule
+ * A linear memory whose every token takes its gradient at the memory as it stands, decayed, and
+ * whose queries read it after the write (titans_mem_forward's chunks take it at the chunk-start
+ * weights). Per unit, W [d, d] fp32 in the column convention M(x) = W x:
+ *   A_t = exp(g_t) W_{t-1},  e_t = beta_t (v_t - A_t k_t),  W_t = A_t + e_t k_t^T,  y_t = W_t q_t.
+ * g <= 0 is the log of what is retained (log(1 - alpha) of the other memories; -infinity forgets
+ * all), beta the writing strength. H value heads share Hk key/query heads: head h reads key head
+ * h / (H / Hk). The calls keep no handle: they read the configuration that they are given, run on
+ * the current device, and two calls may run at the same time as long as they share no workspace
+ * and no output. No output may overlap an input. */
+typedef struct {
+    int d;              /* width of keys and values: 64 or 128 */
+    titans_mode_t mode; /* dtype of k, q, v, attn, y, dy, dk, dq, dv; the state and the gates are fp32 */
+    int B, H;           /* batch and value heads: B*H units */
+    int Hk;             /* key/query heads; divides H */
+} titans_delta_config;
+
+/*
+ * T tokens of every unit.
+ *   k, q     [B, Hk, T, d]; v, y [B, H, T, d]; g, beta [B, H, T] fp32 (4-byte aligned)
+ *   lengths  [B] int32 or NULL (all T): tokens of each sequence, clamped to 0..T; the tokens behind
+ *            them leave the state alone and have y = 0, whatever they hold
+ *   W        [B, H, d, d] fp32, read at entry and overwritten with the state after the last token
+ *   attn     [B, H, T, d] or NULL: the attention branch's output; y = attn * sigmoid(W_t q_t) then
+ *            (as titans_mem_forward_gated)
+ *   workspace  device memory of titans_delta_workspace_bytes(cfg, T, 0) bytes, 16-byte aligned
+ *            (NULL where that is 0); nothing in it is kept between calls
+ * T >= 1 and T * d < 2^31. fp32 arithmetic, or tensor-core products of operands split into fp16
+ * pieces that together hold 22 bits.
+ */
+titans_status_t titans_delta_forward(const titans_delta_config *cfg, const void *k, const void *q, const void *v,
+                                     const float *g, const float *beta, const int *lengths, long T, float *W,
+                                     const void *attn, void *y, void *workspace, size_t workspace_bytes,
+                                     void *stream);
+
+/* Bytes of workspace that titans_delta_forward (call = 0) or titans_delta_backward (call = 1) needs for
+ * T tokens. (size_t)-1 for a bad configuration, T or call, with a message in titans_last_error_string(). */
+size_t titans_delta_workspace_bytes(const titans_delta_config *cfg, long T, int call);
+
+/* One token of every unit: k, q [B, Hk, d]; v, attn (or NULL), y [B, H, d]; g, beta [B, H]; W as above. */
+titans_status_t titans_delta_step(const titans_delta_config *cfg, const void *k, const void *q, const void *v,
+                                  const float *g, const float *beta, float *W, const void *attn, void *y,
+                                  void *stream);
+
+/*
+ * Gradients of <dy, y> + <dW, W_T> for titans_delta_forward without attn, W being the state it starts
+ * from (read only) and dW [B, H, d, d] fp32 the adjoint of the state it ends with (NULL = zero):
+ *   dk, dq [B, Hk, T, d], summed over the value heads that share them, dv [B, H, T, d];
+ *   dg, dbeta [B, H, T] fp32; dW0 [B, H, d, d] fp32.
+ * Gradients of the tokens behind `lengths` are zero, and dy is not read there.
+ * workspace as in titans_delta_forward, with call = 1. dk, dq, dv in the mode's dtype.
+ */
+titans_status_t titans_delta_backward(const titans_delta_config *cfg, const void *k, const void *q, const void *v,
+                                      const float *g, const float *beta, const int *lengths, long T,
+                                      const float *W, const void *dy, const float *dW, void *dk, void *dq,
+                                      void *dv, float *dg, float *dbeta, float *dW0, void *workspace,
+                                      size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------ paged key/value cache
+ * The attention branch beside a memory: keys and values of B sequences in pages of `page` tokens,
+ * attention of a chunk of new tokens (one or more) over them, in bf16. Its output is what the gated
+ * calls above take as `attn`.
+ * Token p of sequence b lies in page table[b, p / page], slot p % page. */
+typedef enum {
+    TITANS_CACHE_BF16 = 0,
+    TITANS_CACHE_E4M3 = 1 /* 8-bit floats with one power-of-two scale per token and head: the smallest
+                           * 2^e with max |x| <= 448 * 2^e over the finite x (e >= -117; 1 where all are 0).
+                           * Infinities become +-448 * 2^e, NaN stays NaN. */
+} titans_cache_type_t;
+
+typedef struct {
+    int d;                    /* width of a head: 64 or 128 */
+    titans_cache_type_t type;
+    int B, H, Hkv;            /* sequences, query heads, key/value heads (Hkv divides H) */
+    int page;                 /* tokens of a page: 16, 32, 64 or 128 */
+    int num_pages;            /* pages of the pool */
+    int max_pages;            /* entries of a sequence's row of the page table */
+} titans_cache_config;
+
+/* The pool, owned by the caller: k, v [num_pages, Hkv, page, d] bf16 or e4m3 bytes, 16-byte aligned;
+ * k_scale, v_scale [num_pages, Hkv, page] fp32 (e4m3 only, else NULL). */
+typedef struct {
+    void *k, *v;
+    float *k_scale, *v_scale;
+} titans_cache_pages;
+
+typedef struct titans_cache *titans_cache_t;
+
+/* Validates the configuration and allocates the handle and its device status word on the current
+ * device, the one that its calls have to be made on. A token whose page is missing (its index is
+ * max_pages or more, or its table entry is outside 0..num_pages-1) is skipped by append, read as
+ * zeros by read and invisible to attend, and recorded in the status word. */
+titans_status_t titans_cache_init(const titans_cache_config *cfg, titans_cache_t *out);
+titans_status_t titans_cache_destroy(titans_cache_t c);
+/* As titans_mem_sync_status. */
+titans_status_t titans_cache_sync_status(titans_cache_t c, void *stream);
+
+/*
+ * Writes T new tokens of every sequence at positions starts[b] + t, t < counts[b].
+ *   k, v    [B, Hkv, T, d] bf16
+ *   table   [B, max_pages] int32; starts [B] int32 >= 0; counts [B] int32 or NULL (all T), clamped to 0..T
+ * Nothing else in the pool is touched. Where two tokens of a call share a slot, either may be kept.
+ */
+titans_status_t titans_cache_append(titans_cache_t c, const void *k, const void *v, long T,
+                                    const titans_cache_pages *pages, const int *table, const int *starts,
+                                    const int *counts, void *stream);
+
+/* Reads positions starts[b] + t, t < counts[b], back into k, v [B, Hkv, T, d] bf16 (an e4m3 value times
+ * its scale is exact in bf16); zeros for t >= counts[b]. */
+titans_status_t titans_cache_read(titans_cache_t c, const titans_cache_pages *pages, const int *table,
+                                  const int *starts, const int *counts, long T, void *k, void *v, void *stream);
+
+/*
+ * Attention of the chunk that append wrote with the same starts and counts (or of any queries at those
+ * positions). Query t of sequence b stands at p = starts[b] + t and sees the keys j <= p; with
+ * window > 0 only those with j > p - window or j < sinks (persistent tokens at the front).
+ *   q, o  [B, H, T, d] bf16; head h reads key/value head h / (H / Hkv)
+ *   scale  factor of q.k before the softmax, finite
+ *   workspace  titans_cache_attend_workspace_bytes(c, T) bytes, 16-byte aligned (NULL where that is 0)
+ * A row that sees no key, and the rows t >= counts[b], are zeros. A key that a row does not see does not
+ * reach it, infinities and NaN included. Scores, softmax and sums in fp32, the weights rounded to bf16
+ * for their product with v.
+ */
+titans_status_t titans_cache_attend(titans_cache_t c, const void *q, long T, const titans_cache_pages *pages,
+                                    const int *table, const int *starts, const int *counts, int window,
+                                    int sinks, float scale, void *o, void *workspace, size_t workspace_bytes,
+                                    void *stream);
+size_t titans_cache_attend_workspace_bytes(titans_cache_t c, long T);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,152 @@
+"""The gated delta rule on the GPU against the recurrence in 64 bits (delta_ref)."""
+import pytest
+import torch
+
+import delta_ref
+from delta_ref import assert_close
+from titans_long_term_b200 import DeltaMemory, Memory, PagedCache
+
+pytestmark = pytest.mark.gpu
+
+
+def make(B, H, Hk, T, d, mode, **kw):
+    x = delta_ref.inputs(B, H, Hk, T, d, mode, device="cuda", **kw)
+    return DeltaMemory(d, mode, B, H, k_heads=Hk), x
+
+
+def call(m, x, gated=False, lengths=True, **kw):
+    W = x["W"].clone()
+    y = m.forward(x["k"], x["q"], x["v"], x["g"], x["beta"], {"W": W}, lengths=x["lengths"] if lengths else None,
+                  attn=x["attn"] if gated else None, **kw)
+    return y, W
+
+
+@pytest.mark.parametrize("mode", ["bf16", "fp32"])
+@pytest.mark.parametrize("B,H,Hk,T,d", [
+    (1, 1, 1, 1, 64), (2, 4, 4, 2, 128), (1, 2, 2, 15, 64), (1, 2, 1, 31, 128), (2, 3, 1, 63, 64), (1, 4, 2, 64, 128),
+    (1, 2, 2, 65, 64), (2, 2, 1, 130, 128), (3, 6, 2, 257, 64), (1, 1, 1, 700, 128), (5, 4, 4, 333, 64)])
+def test_forward(B, H, Hk, T, d, mode):
+    m, x = make(B, H, Hk, T, d, mode, seed=T)
+    y, W = call(m, x)
+    ry, rW = delta_ref.forward(x)
+    assert_close("y", y, ry, mode)
+    assert_close("W", W, rW, "fp32")
+
+
+@pytest.mark.parametrize("mode", ["bf16", "fp32"])
+@pytest.mark.parametrize("B,H,Hk,T,d", [(5, 2, 1, 3, 64), (5, 2, 2, 150, 128), (5, 3, 3, 200, 64)])
+def test_forward_ragged_gated(B, H, Hk, T, d, mode):
+    """Lengths of 0, 1, T / 2, T - 1 and T; what stands behind them, NaN too, reaches nothing, and y = 0 there."""
+    m, x = make(B, H, Hk, T, d, mode, seed=T, ragged=True)
+    ry, rW = delta_ref.forward(x, gated=True)
+    for b, n in enumerate(x["lengths"].tolist()):
+        for name in ("k", "q", "v", "g", "beta", "attn"):
+            x[name][b, :, n:] = float("nan")
+    y, W = call(m, x, gated=True)
+    assert_close("y", y, ry, mode)
+    assert_close("W", W, rW, "fp32")
+    for b, n in enumerate(x["lengths"].tolist()):
+        assert (y[b, :, n:] == 0).all()
+    assert torch.equal(W[1], x["W"][1])  # length 0: untouched
+
+
+@pytest.mark.parametrize("T", [7, 90, 300])
+@pytest.mark.parametrize("mode", ["bf16", "fp32"])
+def test_forward_resets_and_silent_tokens(T, mode):
+    """g = -inf forgets everything, beta = 0 writes nothing."""
+    m, x = make(2, 2, 2, T, 64, mode, seed=T, reset=True)
+    y, W = call(m, x)
+    ry, rW = delta_ref.forward(x)
+    assert_close("y", y, ry, mode)
+    assert_close("W", W, rW, "fp32")
+
+
+@pytest.mark.parametrize("change", ["large values", "small values", "small keys", "strong decay", "same key"])
+def test_forward_ranges(change):
+    m, x = make(1, 2, 2, 200, 64, "fp32", seed=5)
+    if change == "large values":
+        x["v"] *= 1e12
+    elif change == "small values":
+        x["v"] *= 1e-12
+        x["W"] *= 1e-12
+    elif change == "small keys":
+        x["k"] *= 1e-5
+    elif change == "strong decay":
+        x["g"] *= 400
+    else:  # every token overwrites the same direction
+        x["k"][:] = x["k"][:, :, :1]
+        x["beta"][:] = 1
+    y, W = call(m, x)
+    ry, rW = delta_ref.forward(x)
+    assert_close("y", y, ry, "fp32")
+    assert_close("W", W, rW, "fp32")
+
+
+def test_forward_in_two_calls():
+    """A stream cut at any token goes on from its state."""
+    m, x = make(2, 2, 2, 301, 64, "fp32", seed=1)
+    ry, rW = delta_ref.forward(x)
+    state = {"W": x["W"].clone()}
+    ys = []
+    for lo, hi in ((0, 77), (77, 78), (78, 301)):
+        z = {n: x[n][:, :, lo:hi].contiguous() for n in ("k", "q", "v", "g", "beta")}
+        ys.append(m.forward(*z.values(), state))
+    assert_close("y", torch.cat(ys, 2), ry, "fp32")
+    assert_close("W", state["W"], rW, "fp32")
+
+
+@pytest.mark.parametrize("mode", ["bf16", "fp32"])
+@pytest.mark.parametrize("B,H,Hk,d", [(1, 1, 1, 64), (3, 4, 2, 128), (2, 5, 5, 64)])
+def test_step(B, H, Hk, d, mode):
+    m, x = make(B, H, Hk, 3, d, mode, seed=d + B)
+    ry, rW = delta_ref.forward(x)
+    go, _ = delta_ref.forward(x, gated=True)
+    state = {"W": x["W"].clone()}
+    for t in range(3):
+        z = {n: x[n][:, :, t].contiguous() for n in ("k", "q", "v", "g", "beta", "attn")}
+        attn = z.pop("attn") if t == 1 else (z.pop("attn"), None)[1]
+        y = m.step(*z.values(), state, attn=attn)
+        assert_close("y", y[:, :, None], (go if t == 1 else ry)[:, :, t, None], mode)
+    assert_close("W", state["W"], rW, "fp32")
+
+
+def test_other_stream_and_outputs():
+    """A call on its own stream, with its own output, equals the plain one bit for bit; so does one replayed from
+    a graph with new inputs in the captured tensors."""
+    m, x = make(2, 4, 2, 150, 64, "bf16", seed=9)
+    y0, W0 = call(m, x)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    y1 = torch.full_like(x["v"], float("nan"))
+    _, W1 = call(m, x, y=y1, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(y0, y1) and torch.equal(W0, W1)
+    z = {n: t.clone() for n, t in x.items()}
+    W = {"W": z["W"].clone()}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y2 = m.forward(z["k"], z["q"], z["v"], z["g"], z["beta"], W, lengths=z["lengths"])
+    other = delta_ref.inputs(2, 4, 2, 150, 64, "bf16", device="cuda", seed=10)
+    for new in (other, x):
+        for n in z:
+            z[n].copy_(new[n])
+        W["W"].copy_(new["W"])
+        graph.replay()
+        ye, We = call(m, new)
+        assert torch.equal(y2, ye) and torch.equal(W["W"], We)
+
+
+def test_binding_refuses_tensors():
+    m, x = make(1, 2, 1, 8, 64, "bf16")
+    state = {"W": x["W"]}
+    good = [x[n] for n in ("k", "q", "v", "g", "beta")]
+    for i, bad in ((0, x["k"].float()), (0, x["v"]), (1, x["q"].cpu()), (2, x["v"].transpose(-1, -2)), (3, x["g"].double()),
+                   (4, x["beta"][:, :1]), (2, x["v"][:, :, ::2])):
+        args = list(good)
+        args[i] = bad
+        with pytest.raises(ValueError):
+            m.forward(*args, state)
+    with pytest.raises(ValueError, match="lengths"):
+        m.forward(*good, state, lengths=torch.tensor([3], device="cuda"))
+    with pytest.raises(ValueError, match="W"):
+        m.forward(*good, {"W": x["W"].half()})

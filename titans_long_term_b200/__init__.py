@@ -4,6 +4,8 @@ The compute runs in ``libtitans_mem.so`` (hand-written CUDA for sm_100a, C ABI i
 include/titans_mem.h); :mod:`titans_long_term_b200.mem` is its Python binding and
 :mod:`titans_long_term_b200.synth` the seeded synthetic input generator.
 """
+from .cache import PagedCache  # noqa: F401
+from .delta import DeltaMemory  # noqa: F401
 from .mem import Memory, TitansError, new_state  # noqa: F401
 
-__all__ = ["Memory", "TitansError", "new_state"]
+__all__ = ["DeltaMemory", "Memory", "PagedCache", "TitansError", "new_state"]

@@ -1,0 +1,23 @@
+// Host-side launch interface of the paged cache's kernels (not part of the C ABI).
+#pragma once
+#include <cuda_runtime.h>
+
+#include <cstddef>
+
+#include "cache.cuh"
+
+namespace titans {
+
+cudaError_t launch_cache_append(const CacheArgs& a, bool e4m3, const void* k, const void* v, cudaStream_t st);
+cudaError_t launch_cache_read(const CacheArgs& a, bool e4m3, void* k, void* v, cudaStream_t st);
+
+struct AttendArgs {
+    CacheArgs c;
+    const void* q;  // [B, H, T, d] bf16
+    void* o;
+    int window, sinks;
+    float scale;
+};
+cudaError_t launch_cache_attend(const AttendArgs& a, bool e4m3, cudaStream_t st);
+
+}  // namespace titans

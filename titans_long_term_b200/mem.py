@@ -31,7 +31,10 @@ EXPORTED = ["titans_mem_init", "titans_mem_destroy", "titans_mem_forward", "tita
             "titans_mem_path", "titans_mem_sync_status", "titans_last_error_string", "titans_mem_version",
             "titans_mem_forward_noalloc", "titans_mem_forward_host", "titans_mem_forward_gated",
             "titans_mem_step_gated", "titans_mem_init_deep", "titans_mem_forward_deep", "titans_mem_backward",
-            "titans_mem_backward_workspace_bytes", "titans_silu_routes"]
+            "titans_mem_backward_workspace_bytes", "titans_silu_routes", "titans_delta_forward",
+            "titans_delta_workspace_bytes", "titans_delta_step", "titans_delta_backward", "titans_cache_init",
+            "titans_cache_destroy", "titans_cache_sync_status", "titans_cache_append", "titans_cache_read",
+            "titans_cache_attend", "titans_cache_attend_workspace_bytes"]
 
 
 class TitansError(RuntimeError):
@@ -48,6 +51,19 @@ class Config(ctypes.Structure):
 class DeviceBuffers(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("q", ctypes.c_void_p), ("v", ctypes.c_void_p), ("alpha", ctypes.c_void_p),
                 ("eta", ctypes.c_void_p), ("theta", ctypes.c_void_p), ("y", ctypes.c_void_p)]
+
+
+class DeltaConfig(ctypes.Structure):
+    _fields_ = [("d", ctypes.c_int), ("mode", ctypes.c_int), ("B", ctypes.c_int), ("H", ctypes.c_int),
+                ("Hk", ctypes.c_int)]
+
+
+class CacheConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("d", "type", "B", "H", "Hkv", "page", "num_pages", "max_pages")]
+
+
+class CachePages(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")]
 
 
 _lib = None
@@ -80,11 +96,29 @@ def lib():
         L.titans_mem_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, l, i] + [vp] * 20 + [ctypes.c_size_t, vp]
         L.titans_mem_sync_status.argtypes = [vp, vp]
         L.titans_silu_routes.argtypes = [vp, vp, vp, l, vp]
+        delta, sz = ctypes.POINTER(DeltaConfig), ctypes.c_size_t
+        L.titans_delta_forward.argtypes = [delta] + [vp] * 6 + [l] + [vp] * 4 + [sz, vp]
+        L.titans_delta_workspace_bytes.argtypes = [delta, l, i]
+        L.titans_delta_workspace_bytes.restype = sz
+        L.titans_delta_step.argtypes = [delta] + [vp] * 9
+        L.titans_delta_backward.argtypes = [delta] + [vp] * 6 + [l] + [vp] * 10 + [sz, vp]
+        pages = ctypes.POINTER(CachePages)
+        L.titans_cache_init.argtypes = [ctypes.POINTER(CacheConfig), ctypes.POINTER(vp)]
+        L.titans_cache_destroy.argtypes = [vp]
+        L.titans_cache_sync_status.argtypes = [vp, vp]
+        L.titans_cache_append.argtypes = [vp, vp, vp, l, pages, vp, vp, vp, vp]
+        L.titans_cache_read.argtypes = [vp, pages, vp, vp, vp, l, vp, vp, vp]
+        L.titans_cache_attend.argtypes = [vp, vp, l, pages, vp, vp, vp, i, i, ctypes.c_float, vp, vp, sz, vp]
+        L.titans_cache_attend_workspace_bytes.argtypes = [vp, l]
+        L.titans_cache_attend_workspace_bytes.restype = sz
         L.titans_last_error_string.restype = ctypes.c_char_p
         for f in ("titans_mem_init", "titans_mem_destroy", "titans_mem_forward", "titans_mem_step",
                   "titans_mem_path", "titans_mem_sync_status", "titans_mem_version", "titans_mem_forward_noalloc",
                   "titans_mem_forward_host", "titans_mem_forward_gated", "titans_mem_step_gated",
-                  "titans_mem_init_deep", "titans_mem_forward_deep", "titans_mem_backward", "titans_silu_routes"):
+                  "titans_mem_init_deep", "titans_mem_forward_deep", "titans_mem_backward", "titans_silu_routes",
+                  "titans_delta_forward", "titans_delta_step", "titans_delta_backward", "titans_cache_init",
+                  "titans_cache_destroy", "titans_cache_sync_status", "titans_cache_append", "titans_cache_read",
+                  "titans_cache_attend"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
