@@ -31,6 +31,8 @@ titans_status_t check_cfg(const titans_delta_config* c) {
 titans_status_t check_tokens(const titans_delta_config* c, long T) {
     if (T < 1) return fail(TITANS_EINVAL, "T must be >= 1");
     if (T >= (1L << 31) / c->d) return fail(TITANS_EUNSUPPORTED, "T * d must be below 2^31");
+    if ((long)c->B * c->H * ((T + 63) / 64) >= (1L << 31) / 2)
+        return fail(TITANS_EUNSUPPORTED, "B * H * ceil(T / 64) must be below 2^30");
     return TITANS_OK;
 }
 
@@ -77,6 +79,15 @@ titans::DeltaArgs make_args(const titans_delta_config* c, const void* k, const v
     return a;
 }
 
+// Up to this many tokens go one by one, with the state in registers: the chunked path's two launches and its
+// work on 64 tokens cost more there.
+constexpr long kTokens = 16;
+
+long records(const titans_delta_config* c, long T) { return (long)c->B * c->H * ((T + 63) / 64); }
+size_t forward_bytes(const titans_delta_config* c, long T) {
+    return T <= kTokens ? 0 : (size_t)records(c, T) * titans::delta_chunk_bytes();
+}
+
 }  // namespace
 
 extern "C" {
@@ -87,7 +98,7 @@ size_t titans_delta_workspace_bytes(const titans_delta_config* cfg, long T, int 
         fail(TITANS_EINVAL, "call must be 0 (forward) or 1 (backward)");
         return (size_t)-1;
     }
-    return 0;
+    return call ? 0 : forward_bytes(cfg, T);
 }
 
 titans_status_t titans_delta_forward(const titans_delta_config* cfg, const void* k, const void* q, const void* v,
@@ -104,8 +115,11 @@ titans_status_t titans_delta_forward(const titans_delta_config* cfg, const void*
                         {"workspace", workspace, 16, need == 0}};
     if ((s = check_ptrs(args)) != TITANS_OK) return s;
     if (workspace_bytes < need) return fail(TITANS_EINVAL, "workspace is too small");
-    return launched(titans::launch_delta_tokens(make_args(cfg, k, q, v, g, beta, lengths, T, W, attn, y),
-                                                static_cast<cudaStream_t>(stream)));
+    const titans::DeltaArgs a = make_args(cfg, k, q, v, g, beta, lengths, T, W, attn, y);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (T <= kTokens) return launched(titans::launch_delta_tokens(a, st));
+    const cudaError_t e = titans::launch_delta_prepare(a, workspace, st);
+    return launched(e != cudaSuccess ? e : titans::launch_delta_chunks(a, workspace, nullptr, st));
 }
 
 titans_status_t titans_delta_step(const titans_delta_config* cfg, const void* k, const void* q, const void* v,

@@ -1,0 +1,357 @@
+// Gated delta rule, second kernel of the chunked path: the state's way through the chunks, and y.
+//
+// What is serial is the state: each chunk's writes need it (X = V - gamma K W0^T). Rows of W are independent, so
+// a warp keeps sixteen of them in registers as the accumulator of its tensor-core products, which is also the layout
+// of their next A operand: per chunk it takes W0 K^T and W0 Q^T, E^T from N, P E, and adds (l E)^T K to W, without
+// exchanging anything with other warps and without W ever leaving registers. A CTA has 64 rows (32 in
+// fp32 mode at d = 128), four or two such warps, and four producer warps that bring the next chunk's K, Q, V, N
+// and P into a second stage of shared memory meanwhile, the tokens split into fp16 pieces on the way.
+//
+// The serial chain bounds it: with few units most SMs have one warp per tensor core, which runs
+// 448 (d = 64) or 816 (d = 128) m16n8k16 products per chunk one after another.
+#include "delta_common.cuh"
+
+namespace titans {
+namespace {
+
+constexpr int kProducers = 128;
+
+template <int D, int RW, int NP>
+struct Stage {
+    static constexpr int kVLd = RW + 4;  // floats between V's rows: lanes of a fragment hit 32 banks
+    __half k[NP][kC * D], q[NP][kC * D];
+    __half n[2][kC * kC], p[NP][kC * kC];
+    float v[kC * kVLd];
+    float gamma[kC], rest[kC], beta[kC];
+    float scal[8];  // k_scale, q_scale, k_inv, q_inv, n_inv, p_inv
+    float pad[56];
+};
+
+// acc[.] += A B over 16 of k for two n-tiles; the pieces of A are hi, lo and those of B b[0], b[1]: hi hi, lo hi and,
+// where B has a second piece, hi lo.
+template <int NB>
+__device__ __forceinline__ void mma_pieces(float (&acc0)[4], float (&acc1)[4], const uint32_t (&hi)[4],
+                                           const uint32_t (&lo)[4], const uint32_t (&b)[NB][4]) {
+    mma16816(acc0, hi, b[0][0], b[0][1]);
+    mma16816(acc1, hi, b[0][2], b[0][3]);
+    mma16816(acc0, lo, b[0][0], b[0][1]);
+    mma16816(acc1, lo, b[0][2], b[0][3]);
+    if constexpr (NB == 2) {
+        mma16816(acc0, hi, b[1][0], b[1][1]);
+        mma16816(acc1, hi, b[1][2], b[1][3]);
+    }
+}
+
+template <int D, int RW, typename Tok, bool STATES>
+__global__ void __launch_bounds__(RW * 2 + kProducers, 1)
+    delta_chunks_kernel(DeltaArgs a, const DeltaChunk* recs, int chunks, DeltaStates st) {
+    constexpr int NP = sizeof(Tok) == 4 ? 2 : 1, NW = RW / 16, kThreads = NW * 32 + kProducers;
+    using S = Stage<D, RW, NP>;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    S* stages = reinterpret_cast<S*>(smem);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int kSlices = D / RW;
+    const long unit = blockIdx.x / kSlices;
+    const int row_base = (int)(blockIdx.x % kSlices) * RW;
+    const long b = unit / a.H, len = delta_length(a, b);
+    const int used = (int)((len + kC - 1) / kC);
+    const DeltaChunk* rec = recs + unit * chunks;
+    // barriers 1, 2: stage filled; 3, 4: stage free
+
+    if (warp >= NW) {  // ------------------------------------------------ producers
+        const int p = tid - NW * 32;
+        const Tok* k = static_cast<const Tok*>(a.k) + delta_key_head(a, unit) * a.T * D;
+        const Tok* q = static_cast<const Tok*>(a.q) + delta_key_head(a, unit) * a.T * D;
+        const Tok* v = static_cast<const Tok*>(a.v) + unit * a.T * D + row_base;
+        constexpr int VEC = kC * D / 8 / kProducers, VV = kC * RW / 8 / kProducers;
+        for (int c = 0; c < used; ++c) {
+            const long t0 = (long)c * kC;
+            const int n = (int)min((long)kC, len - t0);
+            const DeltaChunk& r = rec[c];
+            S& s = stages[c & 1];
+            // the loads of the tokens are in flight while the stage is still read
+            constexpr int BATCH = sizeof(Tok) == 4 ? 2 : 4;
+            float x[BATCH][8];
+            const float ks = r.k_scale, qs = r.q_scale;
+            if (c >= 2) bar_sync(3 + (c & 1), kThreads);
+            for (int i = p; i < (int)sizeof(r.N) / 16; i += kProducers)
+                cp_async16(smem_u32(s.n) + i * 16, reinterpret_cast<const uint4*>(r.N) + i);
+            if constexpr (!STATES)
+                for (int i = p; i < NP * kC * kC / 8; i += kProducers)
+                    cp_async16(smem_u32(s.p) + i * 16, reinterpret_cast<const uint4*>(r.P) + i);
+            for (int i = p; i < 3 * kC / 4; i += kProducers)
+                cp_async16(smem_u32(s.gamma) + i * 16, reinterpret_cast<const uint4*>(r.gamma) + i);
+            if (p < 6) s.scal[p] = (&r.k_scale)[p];
+#pragma unroll
+            for (int w = 0; w < (STATES ? 1 : 2); ++w) {
+                const Tok* src = (w ? q : k) + t0 * D;
+                const uint32_t base = smem_u32(w ? s.q : s.k);
+#pragma unroll
+                for (int i0 = 0; i0 < VEC; i0 += BATCH) {
+#pragma unroll
+                    for (int i = 0; i < BATCH; ++i) {
+                        const int block = (i0 + i) * kProducers + p;
+                        if (block / (D / 8) < n) {
+                            load8(src + (long)block * 8, x[i]);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) x[i][j] = 0.f;
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < BATCH; ++i) {
+                        const int block = (i0 + i) * kProducers + p;
+                        put8<NP>(base + swz<D>(block / (D / 8), block % (D / 8)), kC * D * 2, x[i], w ? qs : ks);
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < VV; ++i) {
+                const int block = i * kProducers + p, row = block / (RW / 8), col = block % (RW / 8) * 8;
+                if (row < n) {
+                    load8(v + (t0 + row) * D + col, x[0]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[0][j] = 0.f;
+                }
+                store8(s.v + row * S::kVLd + col, x[0]);
+            }
+            cp_async_wait_all();
+            bar_arrive(1 + (c & 1), kThreads);
+        }
+    } else {  // --------------------------------------------------------- sixteen rows of the state a warp
+        const int row = row_base + warp * 16 + (lane >> 2), col2 = 2 * (lane & 3);
+        float w[D / 8][4];
+        float* W = a.W + unit * D * D + (long)row * D + col2;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+            const float2 u = *reinterpret_cast<const float2*>(W + 8 * i);
+            const float2 z = *reinterpret_cast<const float2*>(W + 8 * D + 8 * i);
+            w[i][0] = u.x, w[i][1] = u.y, w[i][2] = z.x, w[i][3] = z.y;
+        }
+        for (int c = 0; c < used; ++c) {
+            S& s = stages[c & 1];
+            if constexpr (STATES) {
+                float* o = st.states + ((unit * chunks + c) * D + row) * D + col2;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    *reinterpret_cast<float2*>(o + 8 * i) = make_float2(w[i][0], w[i][1]);
+                    *reinterpret_cast<float2*>(o + 8 * D + 8 * i) = make_float2(w[i][2], w[i][3]);
+                }
+            }
+            bar_sync(1 + (c & 1), kThreads);
+            const uint32_t ks = smem_u32(s.k), qs = smem_u32(s.q), ns = smem_u32(s.n), ps = smem_u32(s.p);
+            const float k_inv = s.scal[2], q_inv = s.scal[3], n_inv = s.scal[4], p_inv = s.scal[5];
+            float* vs = s.v + warp * 16 + (lane >> 2);
+            // W0 K^T and W0 Q^T
+            float x[8][4] = {}, y[STATES ? 1 : 8][4] = {};
+            float i0, i1;  // inverse scales of the two rows
+            {
+                float top0, top1;
+                row_tops<D / 8>(w, top0, top1);
+                const float s0 = pow2_scale(top0, i0), s1 = pow2_scale(top1, i1);
+#pragma unroll
+                for (int kt = 0; kt < D / 16; ++kt) {
+                    uint32_t hi[4], lo[4];
+                    split_a<D / 8>(w, kt, s0, s1, hi, lo);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t f[NP][4];
+#pragma unroll
+                        for (int e = 0; e < NP; ++e) frag_b<D>(f[e], ks + e * kC * D * 2, j * 16, kt * 16, lane);
+                        mma_pieces<NP>(x[2 * j], x[2 * j + 1], hi, lo, f);
+                        if constexpr (!STATES) {
+#pragma unroll
+                            for (int e = 0; e < NP; ++e) frag_b<D>(f[e], qs + e * kC * D * 2, j * 16, kt * 16, lane);
+                            if constexpr (NP == 2) {
+                                mma_pieces<NP>(y[2 * j], y[2 * j + 1], hi, lo, f);
+                            } else {  // y is rounded to bf16: 11 bits of W are enough
+                                mma16816(y[2 * j], hi, f[0][0], f[0][1]);
+                                mma16816(y[2 * j + 1], hi, f[0][2], f[0][3]);
+                            }
+                        }
+                    }
+                }
+            }
+            // X^T = V^T - gamma W0 K^T (row: value, column: token), and Y's share of W0
+            float r[8][4];  // beta X
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                const int tok = 8 * t + col2;
+                const float2 gm = *reinterpret_cast<const float2*>(s.gamma + tok);
+                const float2 bt = *reinterpret_cast<const float2*>(s.beta + tok);
+                const float* v0 = vs + tok * S::kVLd;
+                x[t][0] = v0[0] - gm.x * k_inv * (x[t][0] * i0);
+                x[t][1] = v0[S::kVLd] - gm.y * k_inv * (x[t][1] * i0);
+                x[t][2] = v0[8] - gm.x * k_inv * (x[t][2] * i1);
+                x[t][3] = v0[S::kVLd + 8] - gm.y * k_inv * (x[t][3] * i1);
+                r[t][0] = bt.x * x[t][0], r[t][1] = bt.y * x[t][1];
+                r[t][2] = bt.x * x[t][2], r[t][3] = bt.y * x[t][3];
+                if constexpr (!STATES) {
+                    y[t][0] *= gm.x * q_inv * i0, y[t][1] *= gm.y * q_inv * i0;
+                    y[t][2] *= gm.x * q_inv * i1, y[t][3] *= gm.y * q_inv * i1;
+                }
+            }
+            // eps^T = X^T - (beta X)^T N^T; N is strictly lower: tokens 16 j + .. see those up to them
+            {
+                float top0, top1;
+                row_tops<8>(r, top0, top1);
+                const float s0 = pow2_scale(top0, i0), s1 = pow2_scale(top1, i1);
+                float acc[8][4] = {};
+#pragma unroll
+                for (int kt = 0; kt < 4; ++kt) {
+                    uint32_t hi[4], lo[4];
+                    split_a<8>(r, kt, s0, s1, hi, lo);
+#pragma unroll
+                    for (int j = kt; j < 4; ++j) {
+                        uint32_t f[2][4];
+                        frag_b<kC>(f[0], ns, j * 16, kt * 16, lane);
+                        frag_b<kC>(f[1], ns + kC * kC * 2, j * 16, kt * 16, lane);
+                        mma_pieces<2>(acc[2 * j], acc[2 * j + 1], hi, lo, f);
+                    }
+                }
+#pragma unroll
+                for (int t = 0; t < 8; ++t) {
+                    x[t][0] -= acc[t][0] * i0 * n_inv, x[t][1] -= acc[t][1] * i0 * n_inv;
+                    x[t][2] -= acc[t][2] * i1 * n_inv, x[t][3] -= acc[t][3] * i1 * n_inv;
+                }
+            }
+            if constexpr (STATES) {
+                float* o = st.eps + ((unit * chunks + c) * kC) * D + row;
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[(long)(8 * t + col2 + (e & 1)) * D + (e >> 1) * 8] = x[t][e];
+            }
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {  // E = beta eps
+                const float2 bt = *reinterpret_cast<const float2*>(s.beta + 8 * t + col2);
+                x[t][0] *= bt.x, x[t][1] *= bt.y, x[t][2] *= bt.x, x[t][3] *= bt.y;
+            }
+            if constexpr (!STATES) {  // Y^T += E^T P^T
+                float top0, top1;
+                row_tops<8>(x, top0, top1);
+                const float s0 = pow2_scale(top0, i0), s1 = pow2_scale(top1, i1);
+                float acc[8][4] = {};
+#pragma unroll
+                for (int kt = 0; kt < 4; ++kt) {
+                    uint32_t hi[4], lo[4];
+                    split_a<8>(x, kt, s0, s1, hi, lo);
+#pragma unroll
+                    for (int j = kt; j < 4; ++j) {
+                        uint32_t f[NP][4];
+#pragma unroll
+                        for (int e = 0; e < NP; ++e) frag_b<kC>(f[e], ps + e * kC * kC * 2, j * 16, kt * 16, lane);
+                        if constexpr (NP == 2) {
+                            mma_pieces<NP>(acc[2 * j], acc[2 * j + 1], hi, lo, f);
+                        } else {
+                            mma16816(acc[2 * j], hi, f[0][0], f[0][1]);
+                            mma16816(acc[2 * j + 1], hi, f[0][2], f[0][3]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int t = 0; t < 8; ++t) {  // into V's place, whose columns only this warp reads
+                    float* v0 = vs + (8 * t + col2) * S::kVLd;
+                    v0[0] = y[t][0] + acc[t][0] * i0 * p_inv;
+                    v0[S::kVLd] = y[t][1] + acc[t][1] * i0 * p_inv;
+                    v0[8] = y[t][2] + acc[t][2] * i1 * p_inv;
+                    v0[S::kVLd + 8] = y[t][3] + acc[t][3] * i1 * p_inv;
+                }
+            }
+            // W = gamma_C W + (l E)^T K
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                const float2 l = *reinterpret_cast<const float2*>(s.rest + 8 * t + col2);
+                x[t][0] *= l.x, x[t][1] *= l.y, x[t][2] *= l.x, x[t][3] *= l.y;
+            }
+            {
+                float top0, top1;
+                row_tops<8>(x, top0, top1);
+                const float s0 = pow2_scale(top0, i0), s1 = pow2_scale(top1, i1);
+                i0 *= k_inv, i1 *= k_inv;
+                const float decay = s.gamma[kC - 1];
+                uint32_t hi[4][4], lo[4][4];
+#pragma unroll
+                for (int kt = 0; kt < 4; ++kt) split_a<8>(x, kt, s0, s1, hi[kt], lo[kt]);
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j) {
+                    float acc[2][4] = {};
+#pragma unroll
+                    for (int kt = 0; kt < 4; ++kt) {
+                        uint32_t f[NP][4];
+#pragma unroll
+                        for (int e = 0; e < NP; ++e) frag_bt<D>(f[e], ks + e * kC * D * 2, j * 16, kt * 16, lane);
+                        mma_pieces<NP>(acc[0], acc[1], hi[kt], lo[kt], f);
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float(&u)[4] = w[2 * j + h];
+                        u[0] = fmaf(u[0], decay, acc[h][0] * i0), u[1] = fmaf(u[1], decay, acc[h][1] * i0);
+                        u[2] = fmaf(u[2], decay, acc[h][2] * i1), u[3] = fmaf(u[3], decay, acc[h][3] * i1);
+                    }
+                }
+            }
+            if constexpr (!STATES) {  // two lanes a token: 32 or 64 bytes of its row
+                __syncwarp();
+                const long t0 = (long)c * kC;
+                const int n = (int)min((long)kC, len - t0);
+                const long at = (unit * a.T + t0) * D + row_base + warp * 16 + (lane & 1) * 8;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int tok = i * 16 + (lane >> 1);
+                    if (tok >= n) continue;
+                    float o[8];
+                    load8(s.v + tok * S::kVLd + warp * 16 + (lane & 1) * 8, o);
+                    if (a.attn) {
+                        float g[8];
+                        load8(static_cast<const Tok*>(a.attn) + at + (long)tok * D, g);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) o[j] = g[j] / (1.f + expf(-o[j]));
+                    }
+                    store8(static_cast<Tok*>(a.y) + at + (long)tok * D, o);
+                }
+            }
+            if (c + 2 < used) bar_arrive(3 + (c & 1), kThreads);
+        }
+        if constexpr (!STATES) {
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                *reinterpret_cast<float2*>(W + 8 * i) = make_float2(w[i][0], w[i][1]);
+                *reinterpret_cast<float2*>(W + 8 * D + 8 * i) = make_float2(w[i][2], w[i][3]);
+            }
+        }
+    }
+    if constexpr (!STATES) {  // nothing is read behind the sequence's end
+        const float zero[8] = {};
+        for (long i = tid; i < (a.T - len) * (RW / 8); i += kThreads)
+            store8(static_cast<Tok*>(a.y) + (unit * a.T + len + i / (RW / 8)) * D + row_base + i % (RW / 8) * 8, zero);
+    }
+}
+
+template <int D, int RW, typename Tok, bool STATES>
+cudaError_t launch(const DeltaArgs& a, const void* recs, const DeltaStates& states, cudaStream_t st) {
+    constexpr size_t bytes = 2 * sizeof(Stage<D, RW, sizeof(Tok) == 4 ? 2 : 1>);
+    static_assert(bytes <= 227 * 1024, "two stages fit an SM");
+    auto* kernel = delta_chunks_kernel<D, RW, Tok, STATES>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)((long)a.B * a.H * (D / RW)), RW * 2 + kProducers, bytes, st>>>(
+        a, static_cast<const DeltaChunk*>(recs), (int)((a.T + kC - 1) / kC), states);
+    return cudaGetLastError();
+}
+
+template <bool STATES>
+cudaError_t launch(const DeltaArgs& a, const void* recs, const DeltaStates& s, cudaStream_t st) {
+    if (a.d == 64)
+        return a.bf16 ? launch<64, 64, __nv_bfloat16, STATES>(a, recs, s, st) : launch<64, 64, float, STATES>(a, recs, s, st);
+    return a.bf16 ? launch<128, 64, __nv_bfloat16, STATES>(a, recs, s, st) : launch<128, 32, float, STATES>(a, recs, s, st);
+}
+
+}  // namespace
+
+cudaError_t launch_delta_chunks(const DeltaArgs& a, const void* chunks, const DeltaStates* states, cudaStream_t st) {
+    return states ? launch<true>(a, chunks, *states, st) : launch<false>(a, chunks, DeltaStates{}, st);
+}
+
+}  // namespace titans
