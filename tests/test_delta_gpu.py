@@ -150,3 +150,98 @@ def test_binding_refuses_tensors():
         m.forward(*good, state, lengths=torch.tensor([3], device="cuda"))
     with pytest.raises(ValueError, match="W"):
         m.forward(*good, {"W": x["W"].half()})
+
+
+def grads(m, x, with_dW=True, **kw):
+    W = x["W"].clone()
+    out = m.backward(x["k"], x["q"], x["v"], x["g"], x["beta"], {"W": W}, x["dy"],
+                     dstate={"W": x["dW"]} if with_dW else None, lengths=x["lengths"], **kw)
+    assert torch.equal(W, x["W"])  # read only
+    return out
+
+
+def check_grads(out, want, mode):
+    for n in ("k", "q", "v"):
+        assert_close(n, out[n], want[n], mode)
+    for n in ("g", "beta", "W"):
+        assert_close(n, out[n], want[n], "fp32")
+
+
+@pytest.mark.parametrize("mode", ["bf16", "fp32"])
+@pytest.mark.parametrize("B,H,Hk,T,d", [
+    (1, 1, 1, 1, 64), (2, 2, 2, 5, 128), (1, 2, 1, 64, 64), (1, 2, 1, 65, 128), (2, 6, 2, 130, 64), (1, 3, 3, 200, 128),
+    (1, 4, 1, 449, 64), (5, 4, 2, 128, 128)])
+def test_backward(B, H, Hk, T, d, mode):
+    m, x = make(B, H, Hk, T, d, mode, seed=T)
+    check_grads(grads(m, x), delta_ref.backward(x), mode)
+
+
+@pytest.mark.parametrize("mode", ["bf16", "fp32"])
+@pytest.mark.parametrize("B,H,Hk,T,d", [(5, 2, 1, 3, 64), (5, 4, 2, 200, 64), (5, 2, 2, 140, 128)])
+def test_backward_ragged(B, H, Hk, T, d, mode):
+    """Gradients behind the lengths are zero, and nothing there is read."""
+    m, x = make(B, H, Hk, T, d, mode, seed=T, ragged=True)
+    want = delta_ref.backward(x)
+    for b, n in enumerate(x["lengths"].tolist()):
+        for name in ("k", "q", "v", "g", "beta", "dy"):
+            x[name][b, :, n:] = float("nan")
+    out = grads(m, x)
+    check_grads(out, want, mode)
+    for b, n in enumerate(x["lengths"].tolist()):
+        for name in ("k", "q", "v", "g", "beta"):
+            assert (out[name][b, :, n:] == 0).all()
+    assert torch.equal(out["W"][1], x["dW"][1])  # length 0
+
+
+@pytest.mark.parametrize("T", [20, 150])
+def test_backward_resets_and_silent_tokens(T):
+    """beta = 0 has its gradient all the same; nothing flows through a decay of 0 (its g gets none)."""
+    m, x = make(2, 2, 2, T, 64, "fp32", seed=T, reset=True)
+    want = delta_ref.backward(x)
+    check_grads(grads(m, x), want, "fp32")
+
+
+def test_backward_without_state_gradient():
+    m, x = make(2, 2, 2, 100, 64, "fp32", seed=8)
+    x["dW"].zero_()
+    check_grads(grads(m, x, with_dW=False), delta_ref.backward(x), "fp32")
+
+
+def test_backward_against_differences():
+    """A step along a random direction changes the forward's value by its product with the gradient: central differences
+    of the fp32 forward, whose value is off by about 2^-22 of |dy| |y|, over a step of 2^-7."""
+    m, x = make(1, 2, 1, 96, 64, "fp32", seed=12)
+
+    def value(z):
+        y, W = call(m, z)
+        return float((y.double() * x["dy"].double()).sum() + (W.double() * x["dW"].double()).sum())
+
+    out = grads(m, x)
+    G = torch.Generator().manual_seed(1)
+    h = 2.0**-7
+    y, _ = call(m, x)
+    noise = 2**-21 * float(x["dy"].norm() * y.norm() + x["dW"].norm() * x["W"].norm()) / h
+    for n in ("k", "q", "v", "g", "beta", "W"):
+        way = torch.randn(x[n].shape, generator=G).cuda()
+        way /= way.norm()
+        d1 = (value({**x, n: x[n] + h * way}) - value({**x, n: x[n] - h * way})) / (2 * h)
+        d2 = (value({**x, n: x[n] + 2 * h * way}) - value({**x, n: x[n] - 2 * h * way})) / (4 * h)
+        change = (4 * d1 - d2) / 3  # the cubic term taken out
+        assert abs(change - float((out[n].double() * way.double()).sum())) <= 4 * noise + abs(d1 - d2), n
+
+
+def test_backward_repeats_and_captures():
+    """The same call twice, on another stream and replayed from a graph: the same bits."""
+    m, x = make(2, 4, 2, 150, 128, "bf16", seed=3)
+    first, s = grads(m, x), torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    second = grads(m, x, stream=s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        third = m.backward(x["k"], x["q"], x["v"], x["g"], x["beta"], {"W": x["W"]}, x["dy"],
+                           dstate={"W": x["dW"]}, lengths=x["lengths"])
+    graph.replay()
+    torch.cuda.synchronize()
+    for n in first:
+        assert torch.equal(first[n], second[n]) and torch.equal(first[n], third[n]), n

@@ -23,9 +23,10 @@ BUILD_DEBUG = os.path.join(HERE, "_build_debug")
 LIB_DEBUG = os.path.join(HERE, "libtitans_mem_debug.so")
 SOURCES = ["api.cu", "chunk_cuda_cores.cu", "chunk_deep_cuda_cores.cu", "chunk_tc_mlp64.cu", "chunk_tc_phased.cu",
            "chunk_tc_deep.cu", "step_cluster.cu", "forward_noalloc.cu", "linear_scan.cu",
-           "linear_backward.cu", "mlp_backward.cu", "mlp_backward_tc.cu", "delta_api.cu", "delta_step.cu", "delta_prepare.cu", "delta_chunks.cu",
+           "linear_backward.cu", "mlp_backward.cu", "mlp_backward_tc.cu", "delta_api.cu", "delta_step.cu", "delta_prepare.cu", "delta_chunks.cu", "delta_adjoint.cu",
+           "delta_grads.cu",
            "cache.cu", "cache_attend.cu"]
-HEADERS = ["kernels.h", "ptx.cuh", "phased_common.cuh", "delta.h", "delta_common.cuh", "cache.h", "cache.cuh"]
+HEADERS = ["kernels.h", "ptx.cuh", "phased_common.cuh", "delta.h", "delta_common.cuh", "delta_stage.cuh", "cache.h", "cache.cuh"]
 NVCC = os.environ.get("NVCC", "nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

@@ -31,4 +31,17 @@ struct DeltaStates {
 };
 cudaError_t launch_delta_chunks(const DeltaArgs& a, const void* chunks, const DeltaStates* states, cudaStream_t st);
 
+struct DeltaGrads {
+    const void* dy;
+    const float* dW;  // adjoint of the final state, NULL: zero
+    void *dk, *dq, *dv;
+    float *dg, *dbeta, *dW0;
+    DeltaStates fwd;    // what launch_delta_chunks left
+    float *adj, *dr;    // every chunk's adjoint of its final state [units][chunks][d][d], and dR [units][chunks][64][d]
+};
+// The adjoint's way back through the chunks: adj, dr, dW0 (delta_adjoint.cu).
+cudaError_t launch_delta_adjoint(const DeltaArgs& a, const void* chunks, const DeltaGrads& g, cudaStream_t st);
+// The tokens' gradients, from the states and adjoints of their chunk (delta_grads.cu).
+cudaError_t launch_delta_grads(const DeltaArgs& a, const void* chunks, const DeltaGrads& g, cudaStream_t st);
+
 }  // namespace titans

@@ -84,6 +84,19 @@ titans::DeltaArgs make_args(const titans_delta_config* c, const void* k, const v
 constexpr long kTokens = 16;
 
 long records(const titans_delta_config* c, long T) { return (long)c->B * c->H * ((T + 63) / 64); }
+struct Backward {  // offsets in the workspace of the backward pass, 1 KiB aligned
+    size_t states, eps, adj, dr, bytes;
+};
+Backward backward_layout(const titans_delta_config* c, long T) {
+    const size_t n = (size_t)records(c, T), matrix = n * c->d * c->d * sizeof(float), tokens = n * 64 * c->d * sizeof(float);
+    Backward b;
+    b.states = n * titans::delta_chunk_bytes();
+    b.eps = b.states + matrix;
+    b.adj = b.eps + tokens;
+    b.dr = b.adj + matrix;
+    b.bytes = b.dr + tokens;
+    return b;
+}
 size_t forward_bytes(const titans_delta_config* c, long T) {
     return T <= kTokens ? 0 : (size_t)records(c, T) * titans::delta_chunk_bytes();
 }
@@ -98,7 +111,7 @@ size_t titans_delta_workspace_bytes(const titans_delta_config* cfg, long T, int 
         fail(TITANS_EINVAL, "call must be 0 (forward) or 1 (backward)");
         return (size_t)-1;
     }
-    return call ? 0 : forward_bytes(cfg, T);
+    return call ? backward_layout(cfg, T).bytes : forward_bytes(cfg, T);
 }
 
 titans_status_t titans_delta_forward(const titans_delta_config* cfg, const void* k, const void* q, const void* v,
@@ -146,9 +159,32 @@ titans_status_t titans_delta_backward(const titans_delta_config* cfg, const void
                         {"g", g, 4, false},    {"beta", beta, 4, false}, {"lengths", lengths, 4, true},
                         {"W", W, 16, false},   {"dy", dy, 16, false},   {"dW", dW, 16, true},
                         {"dk", dk, 16, false}, {"dq", dq, 16, false},   {"dv", dv, 16, false},
-                        {"dg", dg, 4, false},  {"dbeta", dbeta, 4, false}, {"dW0", dW0, 16, false}};
+                        {"dg", dg, 4, false},  {"dbeta", dbeta, 4, false}, {"dW0", dW0, 16, false},
+                        {"workspace", workspace, 16, false}};
     if ((s = check_ptrs(args)) != TITANS_OK) return s;
-    return fail(TITANS_EUNSUPPORTED, "the backward pass is not built yet");
+    const Backward at = backward_layout(cfg, T);
+    if (workspace_bytes < at.bytes) return fail(TITANS_EINVAL, "workspace is too small");
+    char* ws = static_cast<char*>(workspace);
+    const titans::DeltaArgs a =
+        make_args(cfg, k, q, v, g, beta, lengths, T, const_cast<float*>(W), nullptr, nullptr);  // W is only read
+    titans::DeltaGrads o{};
+    o.dy = dy;
+    o.dW = dW;
+    o.dk = dk;
+    o.dq = dq;
+    o.dv = dv;
+    o.dg = dg;
+    o.dbeta = dbeta;
+    o.dW0 = dW0;
+    o.fwd = {reinterpret_cast<float*>(ws + at.states), reinterpret_cast<float*>(ws + at.eps)};
+    o.adj = reinterpret_cast<float*>(ws + at.adj);
+    o.dr = reinterpret_cast<float*>(ws + at.dr);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = titans::launch_delta_prepare(a, ws, st);
+    if (e == cudaSuccess) e = titans::launch_delta_chunks(a, ws, &o.fwd, st);
+    if (e == cudaSuccess) e = titans::launch_delta_adjoint(a, ws, o, st);
+    if (e == cudaSuccess) e = titans::launch_delta_grads(a, ws, o, st);
+    return launched(e);
 }
 
 }  // extern "C"

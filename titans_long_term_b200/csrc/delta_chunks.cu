@@ -9,44 +9,16 @@
 //
 // The serial chain bounds it: with few units most SMs have one warp per tensor core, which runs
 // 448 (d = 64) or 816 (d = 128) m16n8k16 products per chunk one after another.
-#include "delta_common.cuh"
+#include "delta_stage.cuh"
 
 namespace titans {
 namespace {
-
-constexpr int kProducers = 128;
-
-template <int D, int RW, int NP>
-struct Stage {
-    static constexpr int kVLd = RW + 4;  // floats between V's rows: lanes of a fragment hit 32 banks
-    __half k[NP][kC * D], q[NP][kC * D];
-    __half n[2][kC * kC], p[NP][kC * kC];
-    float v[kC * kVLd];
-    float gamma[kC], rest[kC], beta[kC];
-    float scal[8];  // k_scale, q_scale, k_inv, q_inv, n_inv, p_inv
-    float pad[56];
-};
-
-// acc[.] += A B over 16 of k for two n-tiles; the pieces of A are hi, lo and those of B b[0], b[1]: hi hi, lo hi and,
-// where B has a second piece, hi lo.
-template <int NB>
-__device__ __forceinline__ void mma_pieces(float (&acc0)[4], float (&acc1)[4], const uint32_t (&hi)[4],
-                                           const uint32_t (&lo)[4], const uint32_t (&b)[NB][4]) {
-    mma16816(acc0, hi, b[0][0], b[0][1]);
-    mma16816(acc1, hi, b[0][2], b[0][3]);
-    mma16816(acc0, lo, b[0][0], b[0][1]);
-    mma16816(acc1, lo, b[0][2], b[0][3]);
-    if constexpr (NB == 2) {
-        mma16816(acc0, hi, b[1][0], b[1][1]);
-        mma16816(acc1, hi, b[1][2], b[1][3]);
-    }
-}
 
 template <int D, int RW, typename Tok, bool STATES>
 __global__ void __launch_bounds__(RW * 2 + kProducers, 1)
     delta_chunks_kernel(DeltaArgs a, const DeltaChunk* recs, int chunks, DeltaStates st) {
     constexpr int NP = sizeof(Tok) == 4 ? 2 : 1, NW = RW / 16, kThreads = NW * 32 + kProducers;
-    using S = Stage<D, RW, NP>;
+    using S = Stage<D, RW, NP, NP>;
     extern __shared__ __align__(1024) unsigned char smem[];
     S* stages = reinterpret_cast<S*>(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -63,60 +35,10 @@ __global__ void __launch_bounds__(RW * 2 + kProducers, 1)
         const Tok* k = static_cast<const Tok*>(a.k) + delta_key_head(a, unit) * a.T * D;
         const Tok* q = static_cast<const Tok*>(a.q) + delta_key_head(a, unit) * a.T * D;
         const Tok* v = static_cast<const Tok*>(a.v) + unit * a.T * D + row_base;
-        constexpr int VEC = kC * D / 8 / kProducers, VV = kC * RW / 8 / kProducers;
         for (int c = 0; c < used; ++c) {
             const long t0 = (long)c * kC;
-            const int n = (int)min((long)kC, len - t0);
-            const DeltaChunk& r = rec[c];
-            S& s = stages[c & 1];
-            // the loads of the tokens are in flight while the stage is still read
-            constexpr int BATCH = sizeof(Tok) == 4 ? 2 : 4;
-            float x[BATCH][8];
-            const float ks = r.k_scale, qs = r.q_scale;
             if (c >= 2) bar_sync(3 + (c & 1), kThreads);
-            for (int i = p; i < (int)sizeof(r.N) / 16; i += kProducers)
-                cp_async16(smem_u32(s.n) + i * 16, reinterpret_cast<const uint4*>(r.N) + i);
-            if constexpr (!STATES)
-                for (int i = p; i < NP * kC * kC / 8; i += kProducers)
-                    cp_async16(smem_u32(s.p) + i * 16, reinterpret_cast<const uint4*>(r.P) + i);
-            for (int i = p; i < 3 * kC / 4; i += kProducers)
-                cp_async16(smem_u32(s.gamma) + i * 16, reinterpret_cast<const uint4*>(r.gamma) + i);
-            if (p < 6) s.scal[p] = (&r.k_scale)[p];
-#pragma unroll
-            for (int w = 0; w < (STATES ? 1 : 2); ++w) {
-                const Tok* src = (w ? q : k) + t0 * D;
-                const uint32_t base = smem_u32(w ? s.q : s.k);
-#pragma unroll
-                for (int i0 = 0; i0 < VEC; i0 += BATCH) {
-#pragma unroll
-                    for (int i = 0; i < BATCH; ++i) {
-                        const int block = (i0 + i) * kProducers + p;
-                        if (block / (D / 8) < n) {
-                            load8(src + (long)block * 8, x[i]);
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) x[i][j] = 0.f;
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < BATCH; ++i) {
-                        const int block = (i0 + i) * kProducers + p;
-                        put8<NP>(base + swz<D>(block / (D / 8), block % (D / 8)), kC * D * 2, x[i], w ? qs : ks);
-                    }
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < VV; ++i) {
-                const int block = i * kProducers + p, row = block / (RW / 8), col = block % (RW / 8) * 8;
-                if (row < n) {
-                    load8(v + (t0 + row) * D + col, x[0]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x[0][j] = 0.f;
-                }
-                store8(s.v + row * S::kVLd + col, x[0]);
-            }
-            cp_async_wait_all();
+            fill_stage<D, RW, Tok, NP, !STATES>(stages[c & 1], rec[c], k, q, v, t0, (int)min((long)kC, len - t0), p);
             bar_arrive(1 + (c & 1), kThreads);
         }
     } else {  // --------------------------------------------------------- sixteen rows of the state a warp
@@ -331,7 +253,7 @@ __global__ void __launch_bounds__(RW * 2 + kProducers, 1)
 
 template <int D, int RW, typename Tok, bool STATES>
 cudaError_t launch(const DeltaArgs& a, const void* recs, const DeltaStates& states, cudaStream_t st) {
-    constexpr size_t bytes = 2 * sizeof(Stage<D, RW, sizeof(Tok) == 4 ? 2 : 1>);
+    constexpr size_t bytes = 2 * sizeof(Stage<D, RW, sizeof(Tok) == 4 ? 2 : 1, sizeof(Tok) == 4 ? 2 : 1>);
     static_assert(bytes <= 227 * 1024, "two stages fit an SM");
     auto* kernel = delta_chunks_kernel<D, RW, Tok, STATES>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);

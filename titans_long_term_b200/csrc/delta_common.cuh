@@ -33,9 +33,16 @@ struct DeltaChunk {
     float gamma[kC], rest[kC], beta[kC];  // exp(G_i), exp(G_C - G_i), beta_i
     float k_scale, q_scale;               // powers of two that the tiles of K and Q are multiplied by
     float k_inv, q_inv, n_inv, p_inv;     // 1 / the scales
-    float pad[58];
+    float ghi[kC], glo[kC];               // G_i as two floats
+    int zeros[kC];                        // decays of 0 (g = -inf) up to token i, which G leaves out
+    float pad[122];
 };
 static_assert(sizeof(DeltaChunk) % 1024 == 0, "chunks stay 1 KiB aligned");
+
+// exp(G_i - G_j) for j <= i, 0 where a decay of 0 lies between.
+__device__ __forceinline__ float decay_between(const float* ghi, const float* glo, const int* zeros, int i, int j) {
+    return zeros[i] == zeros[j] ? expf((ghi[i] - ghi[j]) + (glo[i] - glo[j])) : 0.f;
+}
 
 // Power of two that brings `top` to [2^14, 2^15), and its inverse. At most 2^114, for tops below 2^-100.
 __device__ __forceinline__ float pow2_scale(float top, float& inv) {
@@ -164,6 +171,28 @@ __device__ __forceinline__ void put8(uint32_t addr, uint32_t lo_offset, const fl
     for (int i = 0; i < 4; ++i) split2(x[2 * i] * s, x[2 * i + 1] * s, h[i], l[i]);
     st_shared_v4(addr, h[0], h[1], h[2], h[3]);
     if constexpr (PIECES == 2) st_shared_v4(addr + lo_offset, l[0], l[1], l[2], l[3]);
+}
+
+// acc += A B for one n-tile, over the pieces: hi hi, lo hi, hi lo where there are such.
+template <int NA, int NB>
+__device__ __forceinline__ void mma_all(float (&acc)[4], const uint32_t (&a)[NA][4], const uint32_t (&b)[NB][2]) {
+    mma16816(acc, a[0], b[0][0], b[0][1]);
+    if constexpr (NA == 2) mma16816(acc, a[1], b[0][0], b[0][1]);
+    if constexpr (NB == 2) mma16816(acc, a[0], b[1][0], b[1][1]);
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+    for (int s = 16; s; s >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, s));
+    return x;
+}
+__device__ __forceinline__ double warp_prefix(double x, int lane) {
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+        const double y = __shfl_up_sync(0xffffffffu, x, s);
+        if (lane >= s) x += y;
+    }
+    return x;
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {

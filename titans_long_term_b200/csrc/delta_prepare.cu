@@ -25,20 +25,6 @@ struct Common {
     float tops[8];
 };
 
-__device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-    for (int s = 16; s; s >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, s));
-    return x;
-}
-__device__ __forceinline__ double warp_prefix(double x, int lane) {
-#pragma unroll
-    for (int s = 1; s < 32; s <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, x, s);
-        if (lane >= s) x += y;
-    }
-    return x;
-}
-
 template <int D, typename Tok>
 __global__ void __launch_bounds__(kThreads) delta_prepare_kernel(DeltaArgs a, DeltaChunk* out, int chunks) {
     using Tiles = Shared<D, Tok>;
@@ -123,7 +109,8 @@ __global__ void __launch_bounds__(kThreads) delta_prepare_kernel(DeltaArgs a, De
             const double G = i ? sum : sum - g[1];
             const int z = i ? zeros : zeros - zero[1];
             const float hi = (float)G;
-            c.ghi[t] = hi, c.glo[t] = (float)(G - hi), c.zeros[t] = z, c.beta[t] = beta[i];
+            o.ghi[t] = c.ghi[t] = hi, o.glo[t] = c.glo[t] = (float)(G - hi), o.zeros[t] = c.zeros[t] = z;
+            c.beta[t] = beta[i];
             o.gamma[t] = z ? 0.f : expf((float)G);
             o.rest[t] = z == all ? expf((float)(last - G)) : 0.f;
             o.beta[t] = beta[i];
@@ -165,8 +152,8 @@ __global__ void __launch_bounds__(kThreads) delta_prepare_kernel(DeltaArgs a, De
         for (int e = 0; e < 4; ++e) {
             const int i = warp * 16 + (lane >> 2) + (e >> 1) * 8, j = 8 * t + 2 * (lane & 3) + (e & 1);
             float m = 0.f, p = 0.f;
-            if (j <= i && c.zeros[i] == c.zeros[j]) {
-                const float d = expf((c.ghi[i] - c.ghi[j]) + (c.glo[i] - c.glo[j])) * s[0];
+            if (j <= i) {
+                const float d = decay_between(c.ghi, c.glo, c.zeros, i, j) * s[0];
                 p = qk[t][e] * s[1] * d;
                 m = j < i ? kk[t][e] * s[0] * d : 0.f;
             }
