@@ -111,6 +111,14 @@ def test_attend_window(T, window, sinks, dtype):
     check(p, T, ints(400 - T, 5), window=window, sinks=sinks)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d,window,sinks,ragged", [(64, 0, 0, True), (128, 0, 0, False), (128, 200, 20, True), (64, 300, 0, False)])
+def test_attend_many_rows(d, window, sinks, ragged, dtype):
+    """Enough rows for two tiles of them a CTA."""
+    p = Pool(4, 12, 6, d, dtype, 32, 900, seed=d)
+    check(p, 560, ints(340, 0, 100, 7), counts=ints(560, 1, 300, 0) if ragged else None, window=window, sinks=sinks)
+
+
 @pytest.mark.parametrize("T", [1, 50, 300])
 def test_attend_padded_batch(T):
     """Counts of 0, 1, T and one beyond T; sequences that hold nothing yet."""

@@ -189,8 +189,8 @@ titans_status_t make_args(titans_cache* c, long T, const titans_cache_pages* pag
     if (!c) return fail(TITANS_EINVAL, "handle is NULL");
     if (!pages) return fail(TITANS_EINVAL, "pages is NULL");
     if (T < 1) return fail(TITANS_EINVAL, "T must be >= 1");
-    if (T >= (1L << 31) / c->cfg.d || (long)c->cfg.B * c->cfg.H * T >= (1L << 34))
-        return fail(TITANS_EUNSUPPORTED, "T * d must be below 2^31 and B * H * T below 2^34");
+    if (T >= (1L << 31) / c->cfg.d || (long)c->cfg.B * c->cfg.H * T >= (1L << 31))
+        return fail(TITANS_EUNSUPPORTED, "T * d and B * H * T must be below 2^31");
     int dev = -1;
     const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
@@ -221,6 +221,10 @@ titans_status_t make_args(titans_cache* c, long T, const titans_cache_pages* pag
     a->counts = counts;
     a->status = c->status;
     return TITANS_OK;
+}
+
+int splits(const titans_cache* c, long T) {
+    return titans::attend_splits(c->cfg.B, c->cfg.H, c->cfg.Hkv, T, (long)c->cfg.max_pages * c->cfg.page);
 }
 
 titans_status_t launched(cudaError_t e) { return e == cudaSuccess ? TITANS_OK : cuda_fail(e, "kernel launch"); }
@@ -296,9 +300,8 @@ titans_status_t titans_cache_read(titans_cache_t c, const titans_cache_pages* pa
 }
 
 size_t titans_cache_attend_workspace_bytes(titans_cache_t c, long T) {
-    (void)T;
-    if (!c) return 0;
-    return 0;
+    if (!c || T < 1 || T >= (1L << 31) / c->cfg.d) return 0;  // refused by the call itself
+    return titans::attend_workspace_bytes(c->cfg.B, c->cfg.H, T, c->cfg.d, splits(c, T));
 }
 
 titans_status_t titans_cache_attend(titans_cache_t c, const void* q, long T, const titans_cache_pages* pages,
@@ -319,7 +322,7 @@ titans_status_t titans_cache_attend(titans_cache_t c, const void* q, long T, con
     a.window = window;
     a.sinks = sinks;
     a.scale = scale;
-    return launched(titans::launch_cache_attend(a, c->cfg.type == TITANS_CACHE_E4M3,
+    return launched(titans::launch_cache_attend(a, c->cfg.type == TITANS_CACHE_E4M3, splits(c, T), workspace,
                                                 static_cast<cudaStream_t>(stream)));
 }
 

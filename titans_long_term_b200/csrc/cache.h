@@ -17,7 +17,11 @@ struct AttendArgs {
     void* o;
     int window, sinks;
     float scale;
+    float* part;      // unnormalised outputs of the splits [splits][B, H, T][d]
+    float2* part_ml;  // their maxima (log2) and sums [splits][B, H, T]
 };
-cudaError_t launch_cache_attend(const AttendArgs& a, bool e4m3, cudaStream_t st);
+int attend_splits(int B, int H, int Hkv, long T, long longest);
+size_t attend_workspace_bytes(int B, int H, long T, int d, int splits);
+cudaError_t launch_cache_attend(const AttendArgs& a, bool e4m3, int splits, void* workspace, cudaStream_t st);
 
 }  // namespace titans
