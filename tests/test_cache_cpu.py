@@ -11,7 +11,7 @@ GOOD = dict(d=64, type=0, B=2, H=4, Hkv=2, page=16, num_pages=8, max_pages=4)
 @pytest.mark.parametrize("other,status", [
     (dict(d=80), mem.EUNSUPPORTED), (dict(type=2), mem.EINVAL), (dict(B=0), mem.EINVAL), (dict(Hkv=3), mem.EINVAL),
     (dict(Hkv=0), mem.EINVAL), (dict(page=48), mem.EUNSUPPORTED), (dict(page=8), mem.EUNSUPPORTED),
-    (dict(num_pages=0), mem.EINVAL), (dict(max_pages=-1), mem.EINVAL), (dict(max_pages=1 << 28), mem.EUNSUPPORTED),
+    (dict(num_pages=0), mem.EINVAL), (dict(num_pages=1 << 26), mem.EUNSUPPORTED), (dict(max_pages=1 << 28), mem.EUNSUPPORTED), (dict(max_pages=-1), mem.EINVAL),
     (dict(B=1 << 20, H=64), mem.EINVAL)])
 def test_bad_configurations(other, status):
     c = mem.CacheConfig(*{**GOOD, **other}.values())

@@ -173,6 +173,8 @@ titans_status_t check_cfg(const titans_cache_config* c) {
         return fail(TITANS_EUNSUPPORTED, "page must be 16, 32, 64 or 128");
     if ((long)c->max_pages * c->page >= (1L << 31))
         return fail(TITANS_EUNSUPPORTED, "max_pages * page must be below 2^31");
+    if ((long)c->num_pages * c->Hkv * c->page >= (1L << 31))
+        return fail(TITANS_EUNSUPPORTED, "num_pages * Hkv * page must be below 2^31");
     return TITANS_OK;
 }
 

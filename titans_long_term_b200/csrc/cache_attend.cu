@@ -6,9 +6,10 @@
 //   S = Q K^T       tcgen05, both operands in shared memory, S in TMEM
 //   P = exp2(c S - c m), rounded to bf16 and written over S in TMEM; one thread a row
 //   O += P V        tcgen05, P from TMEM, O in TMEM
-// Four producer warps gather keys and values from their pages into the layouts that the MMA reads, an e4m3 cache
-// converted and scaled on the way (both exact in bf16), what no row sees as zeros. One thread issues the MMAs: with
-// two tiles, the softmax of one runs while the tensor core works for the other.
+// Keys and values come from their pages in the layouts that the MMA reads: a bf16 cache by TMA, one box per page and 64
+// columns, issued by one warp; an e4m3 cache through eight warps that convert and scale it (both exact in
+// bf16). Values that no row of the tile sees are zeroed. One thread issues the MMAs: with two tiles, the softmax of
+// one runs while the tensor core works for the other.
 //
 // O is rescaled in TMEM only when a row's maximum has grown by more than 2^8 since the one its weights refer to: the
 // weights stay below 2^8, which neither bf16 nor the fp32 sums mind, and most tiles need no pass over O.
@@ -122,9 +123,9 @@ template <int D, int NT, int STAGES>
 struct Shared {
     __nv_bfloat16 q[NT][kRows * D];  // per tile D / 64 panels of 64 columns, 128-byte swizzle
     __nv_bfloat16 k[STAGES][kKeys * D], v[STAGES][kKeys * D];
-    uint32_t valid[STAGES][4];  // keys of the stage that exist
-    long at[2][kKeys];          // rows of the pool of the tile being fetched, in turn
-    uint64_t q_full, full[STAGES], empty[STAGES], s_full[NT], p_full[NT], done;
+    uint32_t valid[STAGES][4];  // keys of the stage that some row sees and whose page is there
+    long at[2][kKeys];          // e4m3: rows of the pool of the tile being fetched, in turn
+    uint64_t q_full, full[STAGES], raw[STAGES], empty[STAGES], s_full[NT], p_full[NT], done;
     uint32_t tmem;
     int abort;
 };
@@ -147,8 +148,16 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool there) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+__device__ __forceinline__ void bar_sync_producers(int threads) {
+    asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
+}
+// Box of the tensor map at column x, row y.
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x, int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y)
+        : "memory");
 }
 
 // Eight e4m3 values times their scale as bf16: both steps exact.
@@ -166,8 +175,25 @@ __device__ __forceinline__ uint32_t range_mask(long k0, long lo, long hi) {
     return below_e & ~below_a;
 }
 
+// Largest of 64 values in registers, in four chains.
+__device__ __forceinline__ float max64(const uint32_t (&x)[32], const uint32_t (&y)[32], float top) {
+    float t[4] = {top, top, top, top};
+#pragma unroll
+    for (int e = 0; e < 32; e += 4)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[i] = fmaxf(t[i], fmaxf(__uint_as_float(x[e + i]), __uint_as_float(y[e + i])));
+    return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+}
+
+template <bool E4M3>
+constexpr int kProducerWarps = E4M3 ? 8 : 1;
+template <bool E4M3, int NT>
+constexpr int kThreadsOf = (NT * 4 + 1 + kProducerWarps<E4M3>) * 32;
+
 template <int D, bool E4M3, int NT, int STAGES>
-__global__ void __launch_bounds__(NT * 128 + 160, 1) attend_kernel(AttendArgs a) {
+__global__ void __launch_bounds__(kThreadsOf<E4M3, NT>, 1)
+    attend_kernel(AttendArgs a, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
+    constexpr int kMmaWarp = NT * 4, kProducer0 = NT * 4 + 1;
     using S = Shared<D, NT, STAGES>;
     constexpr int kPanel = kKeys * 128;  // bytes of a panel of 64 columns
     constexpr uint32_t kColumns = NT == 1 ? 256 : 512;
@@ -188,13 +214,14 @@ __global__ void __launch_bounds__(NT * 128 + 160, 1) attend_kernel(AttendArgs a)
     const int first = (int)((long)tiles.count * blockIdx.z / gridDim.z);
     const int last = (int)((long)tiles.count * (blockIdx.z + 1) / gridDim.z), n = last - first;
 
-    if (warp == NT * 4 + 4) {
+    if (warp == kMmaWarp) {
         tmem_alloc(&s.tmem, kColumns);
         tmem_relinquish();
     }
     if (tid == 0) {
         mbar_init(&s.q_full, NT * 128);
-        for (int i = 0; i < STAGES; ++i) mbar_init(&s.full[i], 128), mbar_init(&s.empty[i], 1);
+        for (int i = 0; i < STAGES; ++i)
+            mbar_init(&s.full[i], E4M3 ? kProducerWarps<E4M3> * 32 : 1), mbar_init(&s.raw[i], 1), mbar_init(&s.empty[i], 1);
         for (int i = 0; i < NT; ++i) mbar_init(&s.s_full[i], 1), mbar_init(&s.p_full[i], 128);
         mbar_init(&s.done, 1);
         s.abort = 0;
@@ -246,32 +273,33 @@ __global__ void __launch_bounds__(NT * 128 + 160, 1) attend_kernel(AttendArgs a)
         for (int j = 0; j < n; ++j) {
             const int stage = j % STAGES;
             const long k0 = (long)tiles[first + j] * kKeys;
-            if (!(ok = wait(&s.s_full[tile], j & 1))) break;
+            if (!(ok = __all_sync(0xffffffffu, wait(&s.s_full[tile], j & 1)))) break;
             tc_fence_after();
             if (any) {
                 const bool whole = k0 >= seen.begin && k0 + kKeys - 1 <= p &&
                                    (s.valid[stage][0] & s.valid[stage][1] & s.valid[stage][2] & s.valid[stage][3]) == ~0u;
                 const bool all_whole = __all_sync(0xffffffffu, whole || !live);
                 float top = -INFINITY;
-                uint32_t mask[4];
+                uint32_t mask[4] = {~0u, ~0u, ~0u, ~0u};
+                if (!all_whole) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    mask[i] = ~0u;
-                    if (!all_whole) {
+                    for (int i = 0; i < 4; ++i) {
                         const long kc = k0 + 32 * i;
                         mask[i] = (range_mask(kc, seen.begin, p) | range_mask(kc, 0, seen.sink_end - 1)) & s.valid[stage][i];
                     }
-                    uint32_t r[32];
+                }
+                auto masked = [&](uint32_t(&r)[32], uint32_t m) {  // -infinity where the row does not see the key
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) r[e] = m >> e & 1 ? r[e] : 0xff800000u;
+                };
+#pragma unroll
+                for (int i = 0; i < 4; i += 2) {
+                    uint32_t r[32], u[32];
                     tmem_ld32(ts + 32 * i, r);
+                    tmem_ld32(ts + 32 * i + 32, u);
                     tmem_wait_ld();
-                    if (all_whole) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(r[e]));
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            top = fmaxf(top, mask[i] >> e & 1 ? __uint_as_float(r[e]) : -INFINITY);
-                    }
+                    if (!all_whole) masked(r, mask[i]), masked(u, mask[i + 1]);
+                    top = max64(r, u, top);
                 }
                 const bool grown = j == 0 || (top - m) * scale > kLazy || (m == -INFINITY && top > m);
                 if (__any_sync(0xffffffffu, grown)) {
@@ -292,30 +320,33 @@ __global__ void __launch_bounds__(NT * 128 + 160, 1) attend_kernel(AttendArgs a)
                     }
                 }
                 const float shift = m == -INFINITY ? 0.f : m * scale;
+                float sum[4] = {};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t r[32], w[16];
+                for (int i = 0; i < 4; i += 2) {
+                    uint32_t r[32], u[32], w[16];
                     tmem_ld32(ts + 32 * i, r);
+                    tmem_ld32(ts + 32 * i + 32, u);
                     tmem_wait_ld();
+                    if (!all_whole) masked(r, mask[i]), masked(u, mask[i + 1]);
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        float x = ex2(fmaf(__uint_as_float(r[e]), scale, -shift));
-                        float y = ex2(fmaf(__uint_as_float(r[e + 1]), scale, -shift));
-                        if (!all_whole) {
-                            x = mask[i] >> e & 1 ? x : 0.f;
-                            y = mask[i] >> (e + 1) & 1 ? y : 0.f;
+                    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            const float x = ex2(fmaf(__uint_as_float(h ? u[e] : r[e]), scale, -shift));
+                            const float y = ex2(fmaf(__uint_as_float(h ? u[e + 1] : r[e + 1]), scale, -shift));
+                            sum[e & 2] += x, sum[(e & 2) + 1] += y;
+                            w[e / 2] = pack_bf16x2(x, y);
                         }
-                        l += x + y;
-                        w[e / 2] = pack_bf16x2(x, y);
+                        tmem_st16(ts + 16 * (i + h), w);
                     }
-                    tmem_st16(ts + 16 * i, w);
                 }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 tmem_wait_st();
             }
             tc_fence_before();
             arrive(&s.p_full[tile]);
         }
-        if (n > 0 && ok) ok = wait(&s.done, 0);
+        if (n > 0 && ok) ok = __all_sync(0xffffffffu, wait(&s.done, 0));
         tc_fence_after();
         // The row's output, or its part of it
         const bool partial = gridDim.z > 1;
@@ -381,91 +412,123 @@ __global__ void __launch_bounds__(NT * 128 + 160, 1) attend_kernel(AttendArgs a)
 #pragma unroll
             for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0, 0, 0, 0);
         }
-    } else if (warp < NT * 4 + 4) {  // ----------------------------------------- producers
-        const int i0 = tid - NT * 128;
-        constexpr int LANES = E4M3 ? D / 16 : D / 8, PASSES = kKeys * LANES / 128;  // 16 bytes a lane
-        const int sub = i0 % LANES, group = i0 / LANES;
+    } else if (warp >= kProducer0) {  // ---------------------------------------- producers
         // keys that no row of the CTA sees are neither looked up nor read
         const long see_hi = start + t_hi;
         const Seen lo = seen_by(a, start + t_lo), hi = seen_by(a, see_hi);
-        bool ok = true, pending = false;  // copies begun whose stage has not been announced
-        int stage_of_last = 0;
-        auto landed = [&] {  // the copies of the last stage that was begun
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            fence_proxy_async_smem();
-            arrive(&s.full[stage_of_last]);
-        };
-        for (int j = 0; j < n; ++j) {  // to the end in any case: the barrier below takes all 128 threads
-            const int stage = j % STAGES;
-            const long key = (long)tiles[first + j] * kKeys + i0;
-            long at = -1;
-            if (key <= see_hi && (key >= lo.begin || key < hi.sink_end)) {
-                at = cache_row(c, b, hk, key);
-                if (at < 0) atomicOr(c.status, kStatusMissingPage);
-            }
-            long* rows_at = s.at[j & 1];
-            rows_at[i0] = at;
-            const uint32_t there = __ballot_sync(0xffffffffu, at >= 0);
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-            uint4 kx[E4M3 ? PASSES : 1], vx[E4M3 ? PASSES : 1];
-            float ks[E4M3 ? PASSES : 1], vs[E4M3 ? PASSES : 1];
-            if constexpr (E4M3) {  // in flight while the stage is still read
+        auto needed = [&](long key) { return key <= see_hi && (key >= lo.begin || key < hi.sink_end); };
+        bool ok = true;
+        if constexpr (!E4M3) {  // one warp
+            int raw_uses[STAGES] = {}, last_parity[STAGES];
+            uint64_t* last_bar[STAGES] = {};
+            const int page = 1 << c.page_shift, per_tile = kKeys >> c.page_shift;
+            for (int j = 0; j < n && ok; ++j) {
+                const int stage = j % STAGES;
+                const long k0 = (long)tiles[first + j] * kKeys;
+                // one lane a page: is any of its keys needed, and where does it lie
+                int y = -1;
+                if (lane < per_tile) {
+                    const long key = k0 + ((long)lane << c.page_shift);
+                    // the page's keys that are needed are its first ones (sinks, up to see_hi) or its last ones (window)
+                    if (key <= see_hi && (needed(key) || needed(min(key + page - 1, see_hi)))) {
+                        const long r = cache_row(c, b, hk, key);
+                        if (r >= 0)
+                            y = (int)r;
+                        else
+                            atomicOr(c.status, kStatusMissingPage);
+                    }
+                }
+                const uint32_t pages = __ballot_sync(0xffffffffu, y >= 0);
+                uint32_t valid[4], all = ~0u;  // lane's key 32 i + lane
 #pragma unroll
-                for (int i = 0; i < PASSES; ++i) {
-                    const long r = rows_at[i * (128 / LANES) + group];
+                for (int i = 0; i < 4; ++i) {
+                    const int key = 32 * i + lane;
+                    valid[i] = __ballot_sync(0xffffffffu, needed(k0 + key) && (pages >> (key >> c.page_shift) & 1));
+                    all &= valid[i];
+                }
+                if (j >= STAGES && !(ok = __all_sync(0xffffffffu, wait(&s.empty[stage], (j / STAGES - 1) & 1)))) break;
+                uint64_t* bar = all == ~0u ? &s.full[stage] : &s.raw[stage];
+                last_bar[stage] = bar, last_parity[stage] = (all == ~0u ? j / STAGES : raw_uses[stage]) & 1;
+                if (lane < 4) s.valid[stage][lane] = lane == 0 ? valid[0] : lane == 1 ? valid[1] : lane == 2 ? valid[2] : valid[3];
+                __syncwarp();
+                if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)__popc(pages) * page * D * 4);
+                __syncwarp();
+                if (y >= 0) {
+                    const uint32_t at = (uint32_t)(lane << c.page_shift) * 128;
+#pragma unroll
+                    for (int x = 0; x < D / 64; ++x) {
+                        tma_load_2d(smem_u32(s.k[stage]) + x * kPanel + at, &k_map, bar, x * 64, y);
+                        tma_load_2d(smem_u32(s.v[stage]) + x * kPanel + at, &v_map, bar, x * 64, y);
+                    }
+                }
+                if (all == ~0u) continue;
+                // values that no row sees become zeros before the MMA reads the stage; their scores are masked
+                if (!(ok = __all_sync(0xffffffffu, wait(&s.raw[stage], raw_uses[stage]++ & 1)))) break;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    for (uint32_t dead = ~valid[i]; dead; dead &= dead - 1) {
+                        const int key = 32 * i + __ffs(dead) - 1;
+                        if (lane < D / 8)
+                            st_shared_v4(smem_u32(s.v[stage]) + (lane >> 3) * kPanel + key * 128 + (lane & 7) * 16, 0, 0, 0, 0);
+                    }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) arrive(&s.full[stage]);
+            }
+            if (!ok)  // given up: the copies in flight still land here
+                for (int i = 0; i < STAGES; ++i)
+                    if (last_bar[i]) mbar_wait(last_bar[i], last_parity[i]);
+        } else {
+            constexpr int P = kProducerWarps<E4M3> * 32, LANES = D / 16, PASSES = kKeys * LANES / P;  // 16 bytes a lane
+            const int i0 = tid - kProducer0 * 32, sub = i0 % LANES, group = i0 / LANES;
+            for (int j = 0; j < n; ++j) {  // to the end in any case: the barrier below takes all threads
+                const int stage = j % STAGES;
+                long* rows_at = s.at[j & 1];
+                uint32_t there = 0;
+                if (i0 < kKeys) {
+                    const long key = (long)tiles[first + j] * kKeys + i0;
+                    long at = -1;
+                    if (needed(key)) {
+                        at = cache_row(c, b, hk, key);
+                        if (at < 0) atomicOr(c.status, kStatusMissingPage);
+                    }
+                    rows_at[i0] = at;
+                    there = __ballot_sync(0xffffffffu, at >= 0);
+                }
+                bar_sync_producers(P);
+                uint4 kx[PASSES], vx[PASSES];
+                float ks[PASSES], vs[PASSES];
+#pragma unroll
+                for (int i = 0; i < PASSES; ++i) {  // in flight while the stage is still read
+                    const long r = rows_at[i * (P / LANES) + group];
                     kx[i] = vx[i] = make_uint4(0, 0, 0, 0), ks[i] = vs[i] = 0.f;
                     if (r >= 0) {
                         kx[i] = static_cast<const uint4*>(c.pk)[r * LANES + sub], ks[i] = c.k_scale[r];
                         vx[i] = static_cast<const uint4*>(c.pv)[r * LANES + sub], vs[i] = c.v_scale[r];
                     }
                 }
-            }
-            if (j >= STAGES && ok) {
-                // the last stage's copies are awaited first where the wait for a free stage may depend on them
-                if (pending && !mbar_try_wait(&s.empty[stage], (j / STAGES - 1) & 1)) landed(), pending = false;
-                ok = wait(&s.empty[stage], (j / STAGES - 1) & 1);
-            }
-            if (!ok) continue;
-            if (lane == 0) s.valid[stage][i0 >> 5] = there;
-            const uint32_t kb = smem_u32(s.k[stage]), vb = smem_u32(s.v[stage]);
+                if (j >= STAGES && ok) ok = wait(&s.empty[stage], (j / STAGES - 1) & 1);
+                if (!ok) continue;
+                if (i0 < kKeys && lane == 0) s.valid[stage][i0 >> 5] = there;
+                const uint32_t off = (sub >> 2) * kPanel, col = (sub & 3) * 16;
+                const uint32_t kb = smem_u32(s.k[stage]) + off, vb = smem_u32(s.v[stage]) + off;
 #pragma unroll
-            for (int i = 0; i < PASSES; ++i) {
-                const int r = i * (128 / LANES) + group;
-                if constexpr (E4M3) {
-                    const uint32_t off = (sub >> 2) * kPanel, col = (sub & 3) * 16;
+                for (int i = 0; i < PASSES; ++i) {
+                    const int r = i * (P / LANES) + group;
                     uint4 w = to_bf16(kx[i].x, kx[i].y, ks[i]);
-                    st_shared_v4(kb + off + sw128_off(r, col), w.x, w.y, w.z, w.w);
+                    st_shared_v4(kb + sw128_off(r, col), w.x, w.y, w.z, w.w);
                     w = to_bf16(kx[i].z, kx[i].w, ks[i]);
-                    st_shared_v4(kb + off + sw128_off(r, col + 8), w.x, w.y, w.z, w.w);
+                    st_shared_v4(kb + sw128_off(r, col + 8), w.x, w.y, w.z, w.w);
                     w = to_bf16(vx[i].x, vx[i].y, vs[i]);
-                    st_shared_v4(vb + off + sw128_off(r, col), w.x, w.y, w.z, w.w);
+                    st_shared_v4(vb + sw128_off(r, col), w.x, w.y, w.z, w.w);
                     w = to_bf16(vx[i].z, vx[i].w, vs[i]);
-                    st_shared_v4(vb + off + sw128_off(r, col + 8), w.x, w.y, w.z, w.w);
-                } else {
-                    const long src = rows_at[r];
-                    const uint32_t off = (sub >> 3) * kPanel + sw128_off(r, (sub & 7) * 8);
-                    const long at = src < 0 ? 0 : src * LANES + sub;
-                    cp_async16_zfill(kb + off, static_cast<const uint4*>(c.pk) + at, src >= 0);
-                    cp_async16_zfill(vb + off, static_cast<const uint4*>(c.pv) + at, src >= 0);
+                    st_shared_v4(vb + sw128_off(r, col + 8), w.x, w.y, w.z, w.w);
                 }
-            }
-            if constexpr (E4M3) {
                 fence_proxy_async_smem();
                 arrive(&s.full[stage]);
-            } else {
-                asm volatile("cp.async.commit_group;" ::: "memory");
-                if (pending) {
-                    asm volatile("cp.async.wait_group 1;" ::: "memory");
-                    fence_proxy_async_smem();
-                    arrive(&s.full[stage_of_last]);
-                }
-                pending = true;
-                stage_of_last = stage;
             }
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        if (pending) landed();
-    } else if (lane == 0 && n > 0) {  // ---------------------------------------- the thread that issues the MMAs
+    } else if (warp == kMmaWarp && lane == 0 && n > 0) {  // ---------------------------------------- the thread that issues the MMAs
         const uint32_t id_s = idesc_bf16_f32(128, kKeys, 0, 0), id_o = idesc_bf16_f32(128, D, 0, 1);
         auto scores = [&](int i, int stage) {
             const uint32_t q = smem_u32(s.q[i]), k = smem_u32(s.k[stage]);
@@ -509,7 +572,7 @@ __global__ void __launch_bounds__(NT * 128 + 160, 1) attend_kernel(AttendArgs a)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == NT * 4 + 4) {
+    if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, kColumns);
     }
@@ -545,6 +608,27 @@ __global__ void __launch_bounds__(128) combine_kernel(AttendArgs a, int splits) 
         static_cast<__nv_bfloat16*>(a.o)[row * D + lane * N + i] = __float2bfloat16(acc[i] * inv);
 }
 
+// The bf16 pool as [num_pages * Hkv * page][d], boxes of one page and 64 columns.
+bool encode_pool(CUtensorMap* m, const CacheArgs& c, const void* pool) {
+    typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode encode = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                            cudaSuccess && q == cudaDriverEntryPointSuccess;
+        return ok ? reinterpret_cast<Encode>(p) : nullptr;
+    }();
+    if (!encode) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)c.d, ((cuuint64_t)c.num_pages * c.Hkv) << c.page_shift};
+    const cuuint64_t strides[1] = {(cuuint64_t)c.d * 2};
+    const cuuint32_t box[2] = {64, 1u << c.page_shift}, ones[2] = {1, 1};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(pool), dims, strides, box, ones,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, bool E4M3, int NT>
 cudaError_t launch(const AttendArgs& a, int splits, cudaStream_t st) {
     constexpr int STAGES = D == 64 ? 4 : NT == 1 ? 3 : 2;
@@ -555,7 +639,9 @@ cudaError_t launch(const AttendArgs& a, int splits, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     const long rows = a.c.T * (a.c.H / a.c.Hkv);
     const dim3 grid((unsigned)((rows + NT * kRows - 1) / (NT * kRows) * a.c.B * a.c.Hkv), 1, (unsigned)splits);
-    kernel<<<grid, NT * 128 + 160, sizeof(S), st>>>(a);
+    CUtensorMap k_map{}, v_map{};
+    if (!E4M3 && (!encode_pool(&k_map, a.c, a.c.pk) || !encode_pool(&v_map, a.c, a.c.pv))) return cudaErrorInvalidValue;
+    kernel<<<grid, kThreadsOf<E4M3, NT>, sizeof(S), st>>>(a, k_map, v_map);
     if ((e = cudaGetLastError()) != cudaSuccess || splits == 1) return e;
     combine_kernel<D><<<(unsigned)(((long)a.c.B * a.c.H * a.c.T + 3) / 4), 128, 0, st>>>(a, splits);
     return cudaGetLastError();
