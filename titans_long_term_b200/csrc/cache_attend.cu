@@ -20,6 +20,7 @@
 // With few rows the keys are split over CTAs, each of which leaves its sum, maximum and unnormalised output in the
 // workspace for combine_kernel.
 #include <algorithm>
+#include <type_traits>
 
 #include "cache.h"
 #include "ptx.cuh"
@@ -124,8 +125,10 @@ struct Shared {
     __nv_bfloat16 q[NT][kRows * D];  // per tile D / 64 panels of 64 columns, 128-byte swizzle
     __nv_bfloat16 k[STAGES][kKeys * D], v[STAGES][kKeys * D];
     uint32_t valid[STAGES][4];  // keys of the stage that some row sees and whose page is there
-    long at[2][kKeys];          // e4m3: rows of the pool of the tile being fetched, in turn
-    uint64_t q_full, full[STAGES], raw[STAGES], empty[STAGES], s_full[NT], p_full[NT], done;
+    int at[2][kKeys];           // e4m3: rows of the pool of the tile being fetched, in turn
+    uint64_t q_full, full[STAGES], raw[STAGES], empty[STAGES], s_full[NT], p_full[NT][2], done;
+    float share[NT][2][kRows];  // what the two threads of a row tell one another
+    int bad[NT][kRows];
     uint32_t tmem;
     int abort;
 };
@@ -140,6 +143,12 @@ __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, u
         "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(
             d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate));
+}
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred P;\n elect.sync _|P, 0xffffffff;\n selp.u32 %0, 1, 0, P;\n}" : "=r"(p));
+    return p != 0;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -175,25 +184,48 @@ __device__ __forceinline__ uint32_t range_mask(long k0, long lo, long hi) {
     return below_e & ~below_a;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 // Largest of 64 values in registers, in four chains.
 __device__ __forceinline__ float max64(const uint32_t (&x)[32], const uint32_t (&y)[32], float top) {
     float t[4] = {top, top, top, top};
 #pragma unroll
     for (int e = 0; e < 32; e += 4)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) t[i] = fmaxf(t[i], fmaxf(__uint_as_float(x[e + i]), __uint_as_float(y[e + i])));
+        for (int i = 0; i < 4; ++i) t[i] = max3(t[i], __uint_as_float(x[e + i]), __uint_as_float(y[e + i]));
     return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
 }
 
-template <bool E4M3>
-constexpr int kProducerWarps = E4M3 ? 8 : 1;
+// Warps of a CTA in groups of four: NT * kPair of softmax, one group whose first warp issues the MMAs and whose
+// second one brings a bf16 cache, and for an e4m3 cache two that convert it. kPair = 2: two threads share a row, 64 keys each.
+// Where the launch leaves softmax too few registers it takes over some that the others do not need; what a
+// thread has at launch times the threads covers the new shares (launch() checks it).
 template <bool E4M3, int NT>
-constexpr int kThreadsOf = (NT * 4 + 1 + kProducerWarps<E4M3>) * 32;
+struct Plan {
+    static constexpr int kPair = E4M3 && NT == 2 ? 1 : 2;
+    static constexpr int kSoftmax = NT * kPair * 128, kProducers = E4M3 ? 256 : 32;  // threads
+    static constexpr int kThreads = kSoftmax + 128 + (E4M3 ? 256 : 0);
+    static constexpr int kSoftmaxRegs = NT == 1 ? 0 : E4M3 ? 136 : 104;  // 0: as launched
+    static constexpr int kIssueRegs = E4M3 ? 56 : 64, kProducerRegs = 72;
+    static constexpr int kShares = kSoftmax * kSoftmaxRegs + 128 * kIssueRegs + (E4M3 ? 256 * kProducerRegs : 0);
+};
+template <int REGS>
+__device__ __forceinline__ void registers_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+template <int REGS>
+__device__ __forceinline__ void registers_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
 
 template <int D, bool E4M3, int NT, int STAGES>
-__global__ void __launch_bounds__(kThreadsOf<E4M3, NT>, 1)
+__global__ void __launch_bounds__(Plan<E4M3, NT>::kThreads, 1)
     attend_kernel(AttendArgs a, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
-    constexpr int kMmaWarp = NT * 4, kProducer0 = NT * 4 + 1;
+    using P = Plan<E4M3, NT>;
+    constexpr int kMmaWarp = P::kSoftmax / 32, kProducer0 = E4M3 ? kMmaWarp + 4 : kMmaWarp + 1;
     using S = Shared<D, NT, STAGES>;
     constexpr int kPanel = kKeys * 128;  // bytes of a panel of 64 columns
     constexpr uint32_t kColumns = NT == 1 ? 256 : 512;
@@ -219,10 +251,10 @@ __global__ void __launch_bounds__(kThreadsOf<E4M3, NT>, 1)
         tmem_relinquish();
     }
     if (tid == 0) {
-        mbar_init(&s.q_full, NT * 128);
+        mbar_init(&s.q_full, P::kSoftmax);
         for (int i = 0; i < STAGES; ++i)
-            mbar_init(&s.full[i], E4M3 ? kProducerWarps<E4M3> * 32 : 1), mbar_init(&s.raw[i], 1), mbar_init(&s.empty[i], 1);
-        for (int i = 0; i < NT; ++i) mbar_init(&s.s_full[i], 1), mbar_init(&s.p_full[i], 128);
+            mbar_init(&s.full[i], E4M3 ? P::kProducers : 1), mbar_init(&s.raw[i], 1), mbar_init(&s.empty[i], 1);
+        for (int i = 0; i < NT; ++i) mbar_init(&s.s_full[i], 1), mbar_init(&s.p_full[i][0], P::kPair * 128), mbar_init(&s.p_full[i][1], P::kPair * 128);
         mbar_init(&s.done, 1);
         s.abort = 0;
         fence_mbar_init();
@@ -238,22 +270,31 @@ __global__ void __launch_bounds__(kThreadsOf<E4M3, NT>, 1)
         atomicOr(c.status, kStatusTimeoutMma);
         return false;
     };
+    // The same for a whole warp, whose lanes agree on the outcome.
+    auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        return __all_sync(0xffffffffu, wait(bar, parity)) != 0;
+    };
 
-    if (warp < NT * 4) {  // -------------------------------------------------- softmax: one thread a row
-        const int tile = warp >> 2;
-        const long row = row0 + tid;
+    if (warp < kMmaWarp) {  // --------------------------------------------------- softmax: one or two threads a row
+        if constexpr (P::kSoftmaxRegs > 0) registers_up<P::kSoftmaxRegs>();
+        constexpr bool kTwo = P::kPair == 2;
+        constexpr int kChunks = kTwo ? 2 : 4;          // 32 keys each
+        constexpr int kOut = D / 32 / P::kPair;        // 32 columns of the output each
+        const int tile = warp / (4 * P::kPair), half = kTwo ? (warp >> 2) & 1 : 0, r = (warp & 3) * 32 + lane;
+        const long row = row0 + tile * kRows + r;
         const int t = (int)(row / G), h = hk * G + (int)(row % G);
         const bool live = row < rows && t < count;
         const bool any = __any_sync(0xffffffffu, live);
         const long p = start + t, out = (((long)b * c.H + h) * c.T + t) * D;
         const float sign = a.scale < 0.f ? -1.f : a.scale == 0.f ? 0.f : 1.f;
         const float scale = (a.scale == 0.f ? 1.f : fabsf(a.scale)) * 1.44269504f;
-        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + out;
         if (n > 0) {
             // the row of Q; a scale that is not positive goes into its sign, so that the largest score is the largest weight's
-            const uint32_t base = smem_u32(s.q[tile]), r = tid & 127;
+            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + out;
+            const uint32_t base = smem_u32(s.q[tile]);
 #pragma unroll 4
-            for (int i = 0; i < D / 8; ++i) {
+            for (int i = half * kOut * 4; i < (half + 1) * kOut * 4; ++i) {
                 uint4 u = make_uint4(0, 0, 0, 0);
                 if (live) u = *reinterpret_cast<const uint4*>(q + 8 * i);
                 uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -266,127 +307,170 @@ __global__ void __launch_bounds__(kThreadsOf<E4M3, NT>, 1)
             arrive(&s.q_full);
         }
         const uint32_t lane_base = (uint32_t)(warp & 3) << 21;  // 32 lanes of TMEM a warp
-        const uint32_t ts = tmem + lane_base + tile * 128, to = tmem + lane_base + NT * 128 + tile * D;
+        const uint32_t ts = tmem + lane_base + tile * 128 + half * 64, tp = tmem + lane_base + tile * 128 + half * 32;
+        const uint32_t to = tmem + lane_base + NT * 128 + tile * D + half * kOut * 32;
+        auto pair_sync = [&] {  // the two warps that share 32 rows
+            if constexpr (kTwo) asm volatile("bar.sync %0, 64;" ::"r"(2 + tile * 4 + (warp & 3)) : "memory");
+        };
         const Seen seen = seen_by(a, p);
         float m = -INFINITY, l = 0.f;
         bool ok = true;
         for (int j = 0; j < n; ++j) {
             const int stage = j % STAGES;
-            const long k0 = (long)tiles[first + j] * kKeys;
-            if (!(ok = __all_sync(0xffffffffu, wait(&s.s_full[tile], j & 1)))) break;
-            tc_fence_after();
-            if (any) {
-                const bool whole = k0 >= seen.begin && k0 + kKeys - 1 <= p &&
-                                   (s.valid[stage][0] & s.valid[stage][1] & s.valid[stage][2] & s.valid[stage][3]) == ~0u;
-                const bool all_whole = __all_sync(0xffffffffu, whole || !live);
-                float top = -INFINITY;
-                uint32_t mask[4] = {~0u, ~0u, ~0u, ~0u};
-                if (!all_whole) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const long kc = k0 + 32 * i;
-                        mask[i] = (range_mask(kc, seen.begin, p) | range_mask(kc, 0, seen.sink_end - 1)) & s.valid[stage][i];
-                    }
-                }
-                auto masked = [&](uint32_t(&r)[32], uint32_t m) {  // -infinity where the row does not see the key
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) r[e] = m >> e & 1 ? r[e] : 0xff800000u;
-                };
-#pragma unroll
-                for (int i = 0; i < 4; i += 2) {
-                    uint32_t r[32], u[32];
-                    tmem_ld32(ts + 32 * i, r);
-                    tmem_ld32(ts + 32 * i + 32, u);
-                    tmem_wait_ld();
-                    if (!all_whole) masked(r, mask[i]), masked(u, mask[i + 1]);
-                    top = max64(r, u, top);
-                }
-                const bool grown = j == 0 || (top - m) * scale > kLazy || (m == -INFINITY && top > m);
-                if (__any_sync(0xffffffffu, grown)) {
-                    const float next = fmaxf(m, top);
-                    const float keep = m == next ? 1.f : ex2((m - next) * scale);
-                    m = next;
-                    l *= keep;
-                    if (j > 0) {
-#pragma unroll
-                        for (int i = 0; i < D / 32; ++i) {
-                            uint32_t r[32];
-                            tmem_ld32(to + 32 * i, r);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * keep);
-                            tmem_st32(to + 32 * i, r);
-                        }
-                    }
-                }
-                const float shift = m == -INFINITY ? 0.f : m * scale;
-                float sum[4] = {};
-#pragma unroll
-                for (int i = 0; i < 4; i += 2) {
-                    uint32_t r[32], u[32], w[16];
-                    tmem_ld32(ts + 32 * i, r);
-                    tmem_ld32(ts + 32 * i + 32, u);
-                    tmem_wait_ld();
-                    if (!all_whole) masked(r, mask[i]), masked(u, mask[i + 1]);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            const float x = ex2(fmaf(__uint_as_float(h ? u[e] : r[e]), scale, -shift));
-                            const float y = ex2(fmaf(__uint_as_float(h ? u[e + 1] : r[e + 1]), scale, -shift));
-                            sum[e & 2] += x, sum[(e & 2) + 1] += y;
-                            w[e / 2] = pack_bf16x2(x, y);
-                        }
-                        tmem_st16(ts + 16 * (i + h), w);
-                    }
-                }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                tmem_wait_st();
+            ok = ok && wait_warp(&s.s_full[tile], j & 1);
+            if (!ok) {  // given up, but the other warp of the rows may wait for this one
+                if (any) pair_sync();
+                continue;
             }
-            tc_fence_before();
-            arrive(&s.p_full[tile]);
+            tc_fence_after();
+            if (!any) {
+                tc_fence_before();
+                arrive(&s.p_full[tile][0]);
+                arrive(&s.p_full[tile][1]);
+                continue;
+            }
+            // all of a thread's scores in registers where it has 64, else 64 at a time, read twice
+            uint32_t x[2][32];
+            tmem_ld32(ts, x[0]);
+            tmem_ld32(ts + 32, x[1]);
+            const long k0 = (long)tiles[first + j] * kKeys;
+            const bool whole = k0 >= seen.begin && k0 + kKeys - 1 <= p &&
+                               (s.valid[stage][0] & s.valid[stage][1] & s.valid[stage][2] & s.valid[stage][3]) == ~0u;
+            const bool all_whole = __all_sync(0xffffffffu, whole || !live);
+            uint32_t mask[kChunks];
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) {
+                mask[i] = ~0u;
+                if (!all_whole) {
+                    const long kc = k0 + 32 * (i + 2 * half);
+                    mask[i] = (range_mask(kc, seen.begin, p) | range_mask(kc, 0, seen.sink_end - 1)) & s.valid[stage][i + 2 * half];
+                }
+            }
+            auto masked = [&](uint32_t(&v)[32], uint32_t bits) {  // -infinity where the row does not see the key
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = bits >> e & 1 ? v[e] : 0xff800000u;
+            };
+            float top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < kChunks; i += 2) {
+                if (i > 0) tmem_ld32(ts + 32 * i, x[0]), tmem_ld32(ts + 32 * i + 32, x[1]);
+                tmem_wait_ld();
+                if (!all_whole) masked(x[0], mask[i]), masked(x[1], mask[i + 1]);
+                top = max64(x[0], x[1], top);
+            }
+            if constexpr (kTwo) {  // the other half's; and the scores that P will overwrite have been read
+                s.share[tile][half][r] = top;
+                pair_sync();
+                top = fmaxf(top, s.share[tile][half ^ 1][r]);
+            }
+            const bool grown = j == 0 || (top - m) * scale > kLazy || (m == -INFINITY && top > m);
+            if (__any_sync(0xffffffffu, grown)) {
+                const float next = fmaxf(m, top);
+                const float keep = m == next ? 1.f : ex2((m - next) * scale);
+                m = next;
+                l *= keep;
+                if (j > 0) {
+#pragma unroll
+                    for (int i = 0; i < 2 * kOut; ++i) {
+                        uint32_t o[16];
+                        tmem_ld16(to + 16 * i, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+                        tmem_st16(to + 16 * i, o);
+                    }
+                }
+            }
+            const float shift = m == -INFINITY ? 0.f : m * scale;
+            float sum[4] = {};
+            auto weights = [&](auto whole_tile) {
+#pragma unroll
+                for (int i = 0; i < kChunks; ++i) {
+                    if (!kTwo && i % 2 == 0) {
+                        tmem_ld32(ts + 32 * i, x[0]), tmem_ld32(ts + 32 * i + 32, x[1]);
+                        tmem_wait_ld();
+                        if constexpr (!whole_tile.value) masked(x[0], mask[i]), masked(x[1], mask[i + 1]);
+                    }
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        float y[2];
+#pragma unroll
+                        for (int f = 0; f < 2; ++f) {
+                            const float u = fmaf(__uint_as_float(x[i & 1][e + f]), scale, -shift);
+                            y[f] = ex2(u);
+                            sum[(e & 2) + f] += y[f];
+                        }
+                        w[e / 2] = pack_bf16x2(y[0], y[1]);
+                    }
+                    tmem_st16(tp + 16 * i, w);
+                    if (i == kChunks / 2 - 1 || i == kChunks - 1) {  // half of the weights: the MMA may begin
+                        tmem_wait_st();
+                        tc_fence_before();
+                        arrive(&s.p_full[tile][i == kChunks - 1]);
+                    }
+                }
+            };
+            if (all_whole)
+                weights(std::true_type{});
+            else
+                weights(std::false_type{});
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         }
-        if (n > 0 && ok) ok = __all_sync(0xffffffffu, wait(&s.done, 0));
+        if (n > 0 && ok) ok = wait_warp(&s.done, 0);
         tc_fence_after();
         // The row's output, or its part of it
         const bool partial = gridDim.z > 1;
         const long prow = (((long)blockIdx.z * c.B + b) * c.H + h) * c.T + t;
         float m2 = m * scale;
-        if (any && ok) {
+        if constexpr (kTwo) {
+            pair_sync();  // the last maxima have been read
+            s.share[tile][half][r] = l;
+            pair_sync();
+            l = s.share[tile][0][r] + s.share[tile][1][r];
+        }
+        if (any) {
             const float inv = partial || l == 0.f ? 1.f : 1.f / l;
             bool fine = l == l && l < INFINITY;
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                uint32_t r[32];
-                if (n > 0) {
-                    tmem_ld32(to + 32 * i, r);
+            for (int i = 0; i < kOut; ++i) {
+                uint32_t o[32];
+                if (n > 0 && ok) {
+                    tmem_ld32(to + 32 * i, o);
                     tmem_wait_ld();
                 }
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
-                    float x = n > 0 ? __uint_as_float(r[e]) * inv : 0.f;
-                    fine = fine && fabsf(x) < INFINITY;
-                    r[e] = __float_as_uint(x);
+                    const float v = n > 0 && ok ? __uint_as_float(o[e]) * inv : 0.f;
+                    fine = fine && fabsf(v) < INFINITY;
+                    o[e] = __float_as_uint(v);
                 }
-                if (!live) continue;
+                if (!live || !ok) continue;
+                const int col = (half * kOut + i) * 32;
                 if (partial) {
-                    uint4* dst = reinterpret_cast<uint4*>(a.part + prow * D + 32 * i);
+                    uint4* dst = reinterpret_cast<uint4*>(a.part + prow * D + col);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) dst[e] = make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
+                    for (int e = 0; e < 8; ++e) dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                 } else {
-                    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + out + 32 * i);
+                    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + out + col);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         uint32_t w[4];
 #pragma unroll
                         for (int f = 0; f < 4; ++f)
-                            w[f] = pack_bf16x2(__uint_as_float(r[8 * e + 2 * f]), __uint_as_float(r[8 * e + 2 * f + 1]));
+                            w[f] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * f]), __uint_as_float(o[8 * e + 2 * f + 1]));
                         dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
             }
-            uint32_t again = __ballot_sync(0xffffffffu, live && n > 0 && !fine);
-            __syncwarp();  // what a lane stored above comes before what the others store below
+            fine = fine || !live || n == 0 || !ok;
+            if constexpr (kTwo) {
+                if (half) s.bad[tile][r] = !fine;
+                pair_sync();  // also: what the other half stored comes before what is stored below
+                fine = half || (fine && !s.bad[tile][r]);
+            }
+            uint32_t again = __ballot_sync(0xffffffffu, !fine);
+            __syncwarp();
             while (again) {  // rows that infinities or NaN reached, maybe through keys that they do not see
                 const int who = __ffs(again) - 1;
                 again &= again - 1;
@@ -405,14 +489,17 @@ __global__ void __launch_bounds__(kThreadsOf<E4M3, NT>, 1)
                 }
             }
         }
-        if (partial) {
-            if (row < rows) a.part_ml[prow] = live ? make_float2(m2, l) : make_float2(-INFINITY, 0.f);
-        } else if (row < rows && !live) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + out);
+        if (half == 0) {
+            if (partial) {
+                if (row < rows) a.part_ml[prow] = live ? make_float2(m2, l) : make_float2(-INFINITY, 0.f);
+            } else if (row < rows && !live) {
+                uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + out);
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0, 0, 0, 0);
+            }
         }
-    } else if (warp >= kProducer0) {  // ---------------------------------------- producers
+    } else if (E4M3 ? warp >= kProducer0 : warp == kProducer0) {  // ------------- producers
+        if constexpr (P::kSoftmaxRegs > 0) registers_down<E4M3 ? P::kProducerRegs : P::kIssueRegs>();
         // keys that no row of the CTA sees are neither looked up nor read
         const long see_hi = start + t_hi;
         const Seen lo = seen_by(a, start + t_lo), hi = seen_by(a, see_hi);
@@ -446,7 +533,7 @@ __global__ void __launch_bounds__(kThreadsOf<E4M3, NT>, 1)
                     valid[i] = __ballot_sync(0xffffffffu, needed(k0 + key) && (pages >> (key >> c.page_shift) & 1));
                     all &= valid[i];
                 }
-                if (j >= STAGES && !(ok = __all_sync(0xffffffffu, wait(&s.empty[stage], (j / STAGES - 1) & 1)))) break;
+                if (j >= STAGES && !(ok = wait_warp(&s.empty[stage], (j / STAGES - 1) & 1))) break;
                 uint64_t* bar = all == ~0u ? &s.full[stage] : &s.raw[stage];
                 last_bar[stage] = bar, last_parity[stage] = (all == ~0u ? j / STAGES : raw_uses[stage]) & 1;
                 if (lane < 4) s.valid[stage][lane] = lane == 0 ? valid[0] : lane == 1 ? valid[1] : lane == 2 ? valid[2] : valid[3];
@@ -463,7 +550,7 @@ __global__ void __launch_bounds__(kThreadsOf<E4M3, NT>, 1)
                 }
                 if (all == ~0u) continue;
                 // values that no row sees become zeros before the MMA reads the stage; their scores are masked
-                if (!(ok = __all_sync(0xffffffffu, wait(&s.raw[stage], raw_uses[stage]++ & 1)))) break;
+                if (!(ok = wait_warp(&s.raw[stage], raw_uses[stage]++ & 1))) break;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     for (uint32_t dead = ~valid[i]; dead; dead &= dead - 1) {
@@ -479,11 +566,11 @@ __global__ void __launch_bounds__(kThreadsOf<E4M3, NT>, 1)
                 for (int i = 0; i < STAGES; ++i)
                     if (last_bar[i]) mbar_wait(last_bar[i], last_parity[i]);
         } else {
-            constexpr int P = kProducerWarps<E4M3> * 32, LANES = D / 16, PASSES = kKeys * LANES / P;  // 16 bytes a lane
+            constexpr int LANES = D / 16, PASSES = kKeys * LANES / P::kProducers;  // 16 bytes a lane
             const int i0 = tid - kProducer0 * 32, sub = i0 % LANES, group = i0 / LANES;
             for (int j = 0; j < n; ++j) {  // to the end in any case: the barrier below takes all threads
                 const int stage = j % STAGES;
-                long* rows_at = s.at[j & 1];
+                int* rows_at = s.at[j & 1];
                 uint32_t there = 0;
                 if (i0 < kKeys) {
                     const long key = (long)tiles[first + j] * kKeys + i0;
@@ -492,15 +579,15 @@ __global__ void __launch_bounds__(kThreadsOf<E4M3, NT>, 1)
                         at = cache_row(c, b, hk, key);
                         if (at < 0) atomicOr(c.status, kStatusMissingPage);
                     }
-                    rows_at[i0] = at;
+                    rows_at[i0] = (int)at;
                     there = __ballot_sync(0xffffffffu, at >= 0);
                 }
-                bar_sync_producers(P);
+                bar_sync_producers(P::kProducers);
                 uint4 kx[PASSES], vx[PASSES];
                 float ks[PASSES], vs[PASSES];
 #pragma unroll
                 for (int i = 0; i < PASSES; ++i) {  // in flight while the stage is still read
-                    const long r = rows_at[i * (P / LANES) + group];
+                    const long r = rows_at[i * (P::kProducers / LANES) + group];
                     kx[i] = vx[i] = make_uint4(0, 0, 0, 0), ks[i] = vs[i] = 0.f;
                     if (r >= 0) {
                         kx[i] = static_cast<const uint4*>(c.pk)[r * LANES + sub], ks[i] = c.k_scale[r];
@@ -514,7 +601,7 @@ __global__ void __launch_bounds__(kThreadsOf<E4M3, NT>, 1)
                 const uint32_t kb = smem_u32(s.k[stage]) + off, vb = smem_u32(s.v[stage]) + off;
 #pragma unroll
                 for (int i = 0; i < PASSES; ++i) {
-                    const int r = i * (P / LANES) + group;
+                    const int r = i * (P::kProducers / LANES) + group;
                     uint4 w = to_bf16(kx[i].x, kx[i].y, ks[i]);
                     st_shared_v4(kb + sw128_off(r, col), w.x, w.y, w.z, w.w);
                     w = to_bf16(kx[i].z, kx[i].w, ks[i]);
@@ -528,45 +615,78 @@ __global__ void __launch_bounds__(kThreadsOf<E4M3, NT>, 1)
                 arrive(&s.full[stage]);
             }
         }
-    } else if (warp == kMmaWarp && lane == 0 && n > 0) {  // ---------------------------------------- the thread that issues the MMAs
+    } else if (warp != kMmaWarp) {
+        if constexpr (P::kSoftmaxRegs > 0) registers_down<P::kIssueRegs>();
+    } else {  // ---------------------------------------------------------------- one thread issues the MMAs
+        if constexpr (P::kSoftmaxRegs > 0) registers_down<P::kIssueRegs>();
+        // The whole warp walks the loop and one elected lane issues: what the MMAs take then stays in uniform registers,
+        // without which issuing them takes longer than they do.
+        const int steps = __shfl_sync(0xffffffffu, n, 0);
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const bool lead = elect_one();
         const uint32_t id_s = idesc_bf16_f32(128, kKeys, 0, 0), id_o = idesc_bf16_f32(128, D, 0, 1);
+        // descriptors of the first tile and stage; an offset in bytes is added as its sixteenth
+        const uint64_t q0 = sdesc_sw128(smem_u32(s.q[0]), 16, 1024), kd0 = sdesc_sw128(smem_u32(s.k[0]), 16, 1024);
+        const uint64_t v0 = sdesc_sw128(smem_u32(s.v[0]), kPanel, 1024);
+        constexpr uint32_t kTile = kKeys * D * 2 / 16;
         auto scores = [&](int i, int stage) {
-            const uint32_t q = smem_u32(s.q[i]), k = smem_u32(s.k[stage]);
+            const uint64_t k = kd0 + stage * kTile;
+            if (lead) {
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-                const uint32_t off = (ks >> 2) * kPanel + (ks & 3) * 32;
-                umma_bf16(tmem + i * 128, sdesc_sw128(q + off, 16, 1024), sdesc_sw128(k + off, 16, 1024), id_s, ks > 0);
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint32_t off = ((ks >> 2) * kPanel + (ks & 3) * 32) / 16;
+                    umma_bf16(tm + i * 128, q0 + i * kTile + off, k + off, id_s, ks > 0);
+                }
+                umma_commit(&s.s_full[i]);
             }
-            umma_commit(&s.s_full[i]);
+            __syncwarp();
         };
-        bool ok = wait(&s.q_full, 0) && wait(&s.full[0], 0);
-        if (ok) {
-            tc_fence_after();
-            for (int i = 0; i < NT; ++i) scores(i, 0);
-        }
-        for (int j = 0; j < n && ok; ++j) {
-            const int stage = j % STAGES;
-            for (int i = 0; i < NT && ok; ++i) {
-                if (!(ok = wait(&s.p_full[i], j & 1))) break;
+        bool ok = true;
+        if (steps > 0) {
+            ok = wait_warp(&s.q_full, 0) && wait_warp(&s.full[0], 0);
+            if (ok) {
                 tc_fence_after();
-                const uint32_t v = smem_u32(s.v[stage]);
 #pragma unroll
-                for (int ks = 0; ks < kKeys / 16; ++ks)
-                    umma_bf16_ts(tmem + NT * 128 + i * D, tmem + i * 128 + ks * 8, sdesc_sw128(v + ks * 2048, kPanel, 1024),
-                                 id_o, j > 0 || ks > 0);
-                if (i == NT - 1) umma_commit(j + 1 < n ? &s.empty[stage] : &s.done);
-                if (j + 1 < n) {
+                for (int i = 0; i < NT; ++i) scores(i, 0);
+            }
+        }
+        int stage = 0, next = 1, next_phase = 0;  // of the tile after this one
+        for (int j = 0; j < steps && ok; ++j) {
+            const uint64_t v = v0 + stage * kTile;
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {  // the halves of P in the order in which they are written
+                    ok = ok && wait_warp(&s.p_full[i][part], j & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (lead) {
+#pragma unroll
+                        for (int u = 0; u < kKeys / 32; ++u) {
+                            const int ks = P::kPair == 2 ? (u & 1) + 2 * part + (u >> 1) * 4 : u + 4 * part;
+                            umma_bf16_ts(tm + NT * 128 + i * D, tm + i * 128 + ks * 8, v + ks * 128, id_o,
+                                         part > 0 || u > 0 ? 1u : j > 0);
+                        }
+                        if (part == 1 && i == NT - 1) umma_commit(j + 1 < steps ? &s.empty[stage] : &s.done);
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+                if (j + 1 < steps) {
                     if (i == 0) {
-                        if (!(ok = wait(&s.full[(j + 1) % STAGES], ((j + 1) / STAGES) & 1))) break;
+                        if (!(ok = wait_warp(&s.full[next], next_phase))) break;
                         tc_fence_after();
                     }
-                    scores(i, (j + 1) % STAGES);
+                    scores(i, next);
                 }
             }
+            stage = next;
+            if (++next == STAGES) next = 0, next_phase ^= 1;
         }
         // Nothing of this CTA may still be at work when its TMEM is freed, an aborted pass's MMAs neither.
         if (!ok) {
-            umma_commit(&s.done);
+            if (lead) umma_commit(&s.done);
+            __syncwarp();
             mbar_wait(&s.done, 0);
         }
     }
@@ -639,9 +759,17 @@ cudaError_t launch(const AttendArgs& a, int splits, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     const long rows = a.c.T * (a.c.H / a.c.Hkv);
     const dim3 grid((unsigned)((rows + NT * kRows - 1) / (NT * kRows) * a.c.B * a.c.Hkv), 1, (unsigned)splits);
+    if constexpr (Plan<E4M3, NT>::kSoftmaxRegs > 0) {
+        static const bool enough = [&] {
+            cudaFuncAttributes f;
+            return cudaFuncGetAttributes(&f, kernel) == cudaSuccess &&
+                   f.numRegs * Plan<E4M3, NT>::kThreads >= Plan<E4M3, NT>::kShares;
+        }();
+        if (!enough) return cudaErrorInvalidConfiguration;
+    }
     CUtensorMap k_map{}, v_map{};
     if (!E4M3 && (!encode_pool(&k_map, a.c, a.c.pk) || !encode_pool(&v_map, a.c, a.c.pv))) return cudaErrorInvalidValue;
-    kernel<<<grid, kThreadsOf<E4M3, NT>, sizeof(S), st>>>(a, k_map, v_map);
+    kernel<<<grid, Plan<E4M3, NT>::kThreads, sizeof(S), st>>>(a, k_map, v_map);
     if ((e = cudaGetLastError()) != cudaSuccess || splits == 1) return e;
     combine_kernel<D><<<(unsigned)(((long)a.c.B * a.c.H * a.c.T + 3) / 4), 128, 0, st>>>(a, splits);
     return cudaGetLastError();
