@@ -25,8 +25,8 @@ SOURCES = ["api.cu", "chunk_cuda_cores.cu", "chunk_deep_cuda_cores.cu", "chunk_t
            "chunk_tc_deep.cu", "step_cluster.cu", "forward_noalloc.cu", "linear_scan.cu",
            "linear_backward.cu", "mlp_backward.cu", "mlp_backward_tc.cu", "delta_api.cu", "delta_step.cu", "delta_prepare.cu", "delta_chunks.cu", "delta_adjoint.cu",
            "delta_grads.cu",
-           "cache.cu", "cache_attend.cu"]
-HEADERS = ["kernels.h", "ptx.cuh", "phased_common.cuh", "delta.h", "delta_common.cuh", "delta_stage.cuh", "cache.h", "cache.cuh"]
+           "cache.cu", "cache_attend.cu", "cache_attend_few.cu"]
+HEADERS = ["kernels.h", "ptx.cuh", "phased_common.cuh", "delta.h", "delta_common.cuh", "delta_stage.cuh", "cache.h", "cache.cuh", "cache_attend.cuh"]
 NVCC = os.environ.get("NVCC", "nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

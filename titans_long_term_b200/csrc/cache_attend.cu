@@ -22,7 +22,7 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "cache.h"
+#include "cache_attend.cuh"
 #include "ptx.cuh"
 
 namespace titans {
@@ -31,94 +31,6 @@ namespace {
 constexpr int kKeys = 128;  // keys of a tile
 constexpr int kRows = 128;  // rows of a tile
 constexpr float kLazy = 8.f;
-
-// The keys that the row at position p sees: j < sink_end, or begin <= j <= p.
-struct Seen {
-    long begin, sink_end;
-};
-__device__ __forceinline__ Seen seen_by(const AttendArgs& a, long p) {
-    const long begin = a.window ? max(0L, p - a.window + 1) : 0L;
-    return {begin, min((long)a.sinks, begin)};
-}
-
-// The tiles of keys that rows at positions p0..p1 see: 0..head-1 and tail..end-1.
-struct Tiles {
-    int head, tail, count;
-    __device__ int operator[](int i) const { return i < head ? i : tail + i - head; }
-};
-__device__ __forceinline__ Tiles tiles_of(const AttendArgs& a, long p0, long p1) {
-    Tiles t{0, 0, 0};
-    if (p1 < 0) return t;
-    const long end = p1 / kKeys + 1;
-    t.tail = (int)(seen_by(a, max(p0, 0L)).begin / kKeys);
-    // the last row has the widest view of the sinks: those before its own window
-    t.head = (int)min((long)t.tail, (seen_by(a, p1).sink_end + kKeys - 1) / kKeys);
-    t.count = t.head + (int)end - t.tail;
-    return t;
-}
-
-// N consecutive values of a row of the pool.
-template <int N, bool E4M3>
-__device__ __forceinline__ void load_row(const void* pool, const float* scales, long row, int col, int D, float (&x)[N]) {
-    if constexpr (E4M3) {
-        const float s = scales[row];
-        const uint16_t* p = reinterpret_cast<const uint16_t*>(static_cast<const uint8_t*>(pool) + row * D + col);
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) {
-            const float2 f = e4m3x2_to_float2(p[i]);
-            x[2 * i] = f.x * s;
-            x[2 * i + 1] = f.y * s;
-        }
-    } else {
-        const __nv_bfloat162* p =
-            reinterpret_cast<const __nv_bfloat162*>(static_cast<const __nv_bfloat16*>(pool) + row * D + col);
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) {
-            const float2 f = __bfloat1622float2(p[i]);
-            x[2 * i] = f.x;
-            x[2 * i + 1] = f.y;
-        }
-    }
-}
-
-// One row by one warp, key by key, over tiles first..last-1: m (log2 units), l and D / 32 columns a lane.
-template <int D, bool E4M3>
-__device__ __noinline__ void attend_row(const AttendArgs& a, int b, int hk, const __nv_bfloat16* q, long p, Tiles tiles,
-                                        int first, int last, float& m, float& l, float (&acc)[D / 32]) {
-    constexpr int N = D / 32;
-    const CacheArgs& c = a.c;
-    const int lane = threadIdx.x & 31;
-    const Seen s = seen_by(a, p);
-    float qr[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        qr[i] = __bfloat162float(q[lane * N + i]) * (a.scale * 1.44269504f);
-        acc[i] = 0.f;
-    }
-    m = -INFINITY, l = 0.f;
-    for (int i = first; i < last; ++i) {
-        const long j0 = (long)tiles[i] * kKeys;
-        for (long j = j0; j < j0 + kKeys && j <= p; ++j) {
-            if (j >= s.sink_end && j < s.begin) continue;
-            const long at = cache_row(c, b, hk, j);
-            if (at < 0) continue;
-            float x[N], z = 0.f;
-            load_row<N, E4M3>(c.pk, c.k_scale, at, lane * N, D, x);
-#pragma unroll
-            for (int i = 0; i < N; ++i) z = fmaf(qr[i], x[i], z);
-#pragma unroll
-            for (int i = 16; i; i >>= 1) z += __shfl_xor_sync(0xffffffffu, z, i);
-            const float top = fmaxf(m, z);
-            if (top == -INFINITY && z == z) continue;
-            const float keep = m == top ? 1.f : exp2f(m - top), w = exp2f(z - top);
-            m = top;
-            l = l * keep + w;
-            load_row<N, E4M3>(c.pv, c.v_scale, at, lane * N, D, x);
-#pragma unroll
-            for (int i = 0; i < N; ++i) acc[i] = fmaf(w, x[i], acc[i] * keep);
-        }
-    }
-}
 
 template <int D, int NT, int STAGES>
 struct Shared {
@@ -242,7 +154,7 @@ __global__ void __launch_bounds__(Plan<E4M3, NT>::kThreads, 1)
     const long start = c.starts[b];
     const long t_lo = row0 / G, t_hi = min(min(row0 + NT * kRows, rows) - 1, (long)count * G - 1) / G;
     Tiles tiles{0, 0, 0};
-    if (row0 < (long)count * G) tiles = tiles_of(a, start + t_lo, start + t_hi);
+    if (row0 < (long)count * G) tiles = tiles_of<kKeys>(a, start + t_lo, start + t_hi);
     const int first = (int)((long)tiles.count * blockIdx.z / gridDim.z);
     const int last = (int)((long)tiles.count * (blockIdx.z + 1) / gridDim.z), n = last - first;
 
@@ -477,7 +389,7 @@ __global__ void __launch_bounds__(Plan<E4M3, NT>::kThreads, 1)
                 const long wq = __shfl_sync(0xffffffffu, out, who), wp = __shfl_sync(0xffffffffu, p, who);
                 const long wprow = __shfl_sync(0xffffffffu, prow, who);
                 float rm, rl, acc[D / 32];
-                attend_row<D, E4M3>(a, b, hk, static_cast<const __nv_bfloat16*>(a.q) + wq, wp, tiles, first, last, rm, rl, acc);
+                attend_row<D, E4M3, kKeys>(a, b, hk, static_cast<const __nv_bfloat16*>(a.q) + wq, wp, tiles, first, last, rm, rl, acc);
                 const float rinv = partial || rl == 0.f ? 1.f : 1.f / rl;
                 if (lane == who) m2 = rm, l = rl;
 #pragma unroll
@@ -770,19 +682,21 @@ cudaError_t launch(const AttendArgs& a, int splits, cudaStream_t st) {
     CUtensorMap k_map{}, v_map{};
     if (!E4M3 && (!encode_pool(&k_map, a.c, a.c.pk) || !encode_pool(&v_map, a.c, a.c.pv))) return cudaErrorInvalidValue;
     kernel<<<grid, Plan<E4M3, NT>::kThreads, sizeof(S), st>>>(a, k_map, v_map);
-    if ((e = cudaGetLastError()) != cudaSuccess || splits == 1) return e;
-    combine_kernel<D><<<(unsigned)(((long)a.c.B * a.c.H * a.c.T + 3) / 4), 128, 0, st>>>(a, splits);
     return cudaGetLastError();
+}
+
+// Splits of the keys: enough CTAs for two rounds over the SMs, and no less than four tiles of the longest
+// possible sequence each. The lengths themselves are on the device.
+int tile_splits(int B, int H, int Hkv, long T, long longest) {
+    const long rows = T * (H / Hkv), base = ((rows + kRows - 1) / kRows) * B * Hkv;
+    const long most = std::max(1L, longest / kKeys / 4);
+    return (int)std::max(1L, std::min({most, 2 * 148L / base, 64L}));
 }
 
 }  // namespace
 
-// Splits of the keys: enough CTAs for two rounds over the SMs, and no less than four tiles of the longest
-// possible sequence each. The lengths themselves are on the device.
 int attend_splits(int B, int H, int Hkv, long T, long longest) {
-    const long rows = T * (H / Hkv), base = ((rows + kRows - 1) / kRows) * B * Hkv;
-    const long most = std::max(1L, longest / kKeys / 4);
-    return (int)std::max(1L, std::min({most, 2 * 148L / base, 64L}));
+    return attend_few_rows(H, Hkv, T) ? attend_few_splits(B, Hkv, longest) : tile_splits(B, H, Hkv, T, longest);
 }
 
 size_t attend_workspace_bytes(int B, int H, long T, int d, int splits) {
@@ -794,15 +708,25 @@ cudaError_t launch_cache_attend(const AttendArgs& args, bool e4m3, int splits, v
     const size_t n = (size_t)splits * a.c.B * a.c.H * a.c.T;
     a.part = static_cast<float*>(workspace);
     a.part_ml = reinterpret_cast<float2*>(a.part + (splits > 1 ? n * a.c.d : 0));
-    // Two tiles of rows a CTA where that still leaves a CTA for most SMs
-    const long rows = a.c.T * (a.c.H / a.c.Hkv);
-    const bool two = rows > kRows && (rows + 2 * kRows - 1) / (2 * kRows) * a.c.B * a.c.Hkv * splits >= 100;
-    if (a.c.d == 64) {
-        if (e4m3) return two ? launch<64, true, 2>(a, splits, st) : launch<64, true, 1>(a, splits, st);
-        return two ? launch<64, false, 2>(a, splits, st) : launch<64, false, 1>(a, splits, st);
+    cudaError_t e;
+    if (attend_few_rows(a.c.H, a.c.Hkv, a.c.T)) {
+        e = launch_attend_few(a, e4m3, splits, st);
+    } else {
+        // Two tiles of rows a CTA where that still leaves a CTA for most SMs
+        const long rows = a.c.T * (a.c.H / a.c.Hkv);
+        const bool two = rows > kRows && (rows + 2 * kRows - 1) / (2 * kRows) * a.c.B * a.c.Hkv * splits >= 100;
+        if (a.c.d == 64) {
+            e = e4m3 ? (two ? launch<64, true, 2>(a, splits, st) : launch<64, true, 1>(a, splits, st))
+                     : (two ? launch<64, false, 2>(a, splits, st) : launch<64, false, 1>(a, splits, st));
+        } else {
+            e = e4m3 ? (two ? launch<128, true, 2>(a, splits, st) : launch<128, true, 1>(a, splits, st))
+                     : (two ? launch<128, false, 2>(a, splits, st) : launch<128, false, 1>(a, splits, st));
+        }
     }
-    if (e4m3) return two ? launch<128, true, 2>(a, splits, st) : launch<128, true, 1>(a, splits, st);
-    return two ? launch<128, false, 2>(a, splits, st) : launch<128, false, 1>(a, splits, st);
+    if (e != cudaSuccess || splits == 1) return e;
+    auto* kernel = a.c.d == 64 ? combine_kernel<64> : combine_kernel<128>;
+    kernel<<<(unsigned)(((long)a.c.B * a.c.H * a.c.T + 3) / 4), 128, 0, st>>>(a, splits);
+    return cudaGetLastError();
 }
 
 }  // namespace titans
