@@ -98,14 +98,22 @@ def check(p, T, starts, counts=None, window=0, sinks=0, missing=None, scale=None
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 @pytest.mark.parametrize("B,H,Hkv,d,page,S,T", [
     (1, 1, 1, 64, 16, 1, 1), (2, 4, 4, 128, 16, 40, 1), (3, 6, 2, 64, 32, 300, 7), (1, 4, 1, 128, 64, 700, 130),
-    (2, 3, 3, 64, 128, 513, 65), (1, 8, 2, 128, 16, 257, 257), (1, 20, 1, 64, 64, 1500, 3), (1, 2, 2, 128, 64, 2100, 33)])
+    (2, 3, 3, 64, 128, 513, 65), (1, 8, 2, 128, 16, 257, 257), (1, 20, 1, 64, 64, 1500, 3), (1, 2, 2, 128, 64, 2100, 33),
+    (2, 12, 1, 128, 16, 500, 1), (300, 4, 2, 64, 32, 150, 7), (3, 8, 2, 128, 128, 9000, 2)])
 def test_attend(B, H, Hkv, d, page, S, T, dtype):
     p = Pool(B, H, Hkv, d, dtype, page, S, seed=S)
-    check(p, T, ints(*[S - T - (b * (S - T)) // 3 for b in range(B)]))
+    check(p, T, ints(*[max(0, S - T - (b * (S - T)) // 3) for b in range(B)]))
+
+
+@pytest.mark.parametrize("T", [1, 7, 40])
+def test_attend_few_keys_of_a_long_table(T):
+    """Fewer blocks of keys than the table has room for, sequences of one key, and one whose first queries stand before 0."""
+    p = Pool(5, 4, 2, 64, "bf16", 32, 3000, seed=T)
+    check(p, T, ints(150, 0, 33, -3, 90))
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
-@pytest.mark.parametrize("T,window,sinks", [(1, 1, 0), (1, 100, 4), (90, 17, 0), (90, 64, 16), (200, 150, 300), (200, 1, 1), (33, 5000, 9)])
+@pytest.mark.parametrize("T,window,sinks", [(1, 1, 0), (7, 90, 20), (6, 1, 0), (1, 100, 4), (90, 17, 0), (90, 64, 16), (200, 150, 300), (200, 1, 1), (33, 5000, 9)])
 def test_attend_window(T, window, sinks, dtype):
     p = Pool(2, 4, 2, 64, dtype, 16, 400, seed=T)
     check(p, T, ints(400 - T, 5), window=window, sinks=sinks)
@@ -119,7 +127,7 @@ def test_attend_many_rows(d, window, sinks, ragged, dtype):
     check(p, 560, ints(340, 0, 100, 7), counts=ints(560, 1, 300, 0) if ragged else None, window=window, sinks=sinks)
 
 
-@pytest.mark.parametrize("T", [1, 50, 300])
+@pytest.mark.parametrize("T", [1, 6, 50, 300])
 def test_attend_padded_batch(T):
     """Counts of 0, 1, T and one beyond T; sequences that hold nothing yet."""
     p = Pool(4, 4, 2, 128, "bf16", 32, 600, seed=T)

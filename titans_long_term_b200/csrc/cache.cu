@@ -225,10 +225,6 @@ titans_status_t make_args(titans_cache* c, long T, const titans_cache_pages* pag
     return TITANS_OK;
 }
 
-int splits(const titans_cache* c, long T) {
-    return titans::attend_splits(c->cfg.B, c->cfg.H, c->cfg.Hkv, T, (long)c->cfg.max_pages * c->cfg.page);
-}
-
 titans_status_t launched(cudaError_t e) { return e == cudaSuccess ? TITANS_OK : cuda_fail(e, "kernel launch"); }
 
 }  // namespace
@@ -303,7 +299,8 @@ titans_status_t titans_cache_read(titans_cache_t c, const titans_cache_pages* pa
 
 size_t titans_cache_attend_workspace_bytes(titans_cache_t c, long T) {
     if (!c || T < 1 || T >= (1L << 31) / c->cfg.d) return 0;  // refused by the call itself
-    return titans::attend_workspace_bytes(c->cfg.B, c->cfg.H, T, c->cfg.d, splits(c, T));
+    return titans::attend_workspace_bytes(c->cfg.B, c->cfg.H, c->cfg.Hkv, T, c->cfg.d,
+                                           (long)c->cfg.max_pages * c->cfg.page);
 }
 
 titans_status_t titans_cache_attend(titans_cache_t c, const void* q, long T, const titans_cache_pages* pages,
@@ -324,8 +321,8 @@ titans_status_t titans_cache_attend(titans_cache_t c, const void* q, long T, con
     a.window = window;
     a.sinks = sinks;
     a.scale = scale;
-    return launched(titans::launch_cache_attend(a, c->cfg.type == TITANS_CACHE_E4M3, splits(c, T), workspace,
-                                                static_cast<cudaStream_t>(stream)));
+    return launched(titans::launch_cache_attend(a, c->cfg.type == TITANS_CACHE_E4M3, workspace,
+                                                (long)c->cfg.max_pages * c->cfg.page, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -17,15 +17,16 @@ struct AttendArgs {
     void* o;
     int window, sinks;
     float scale;
-    float* part;      // unnormalised outputs of the splits [splits][B, H, T][d]
-    float2* part_ml;  // their maxima (log2) and sums [splits][B, H, T]
+    float* part;      // workspace: unnormalised outputs of parts of the keys, d each,
+    float2* part_ml;  // their maxima (log2) and sums,
+    long* begins;     // and, for few rows, the first block of each sequence, then the number of blocks
 };
 // Few rows a key/value head (one token of a decode step, say): cache_attend_few.cu.
 bool attend_few_rows(int H, int Hkv, long T);
-int attend_few_splits(int B, int Hkv, long longest);
-cudaError_t launch_attend_few(const AttendArgs& a, bool e4m3, int splits, cudaStream_t st);
-int attend_splits(int B, int H, int Hkv, long T, long longest);
-size_t attend_workspace_bytes(int B, int H, long T, int d, int splits);
-cudaError_t launch_cache_attend(const AttendArgs& a, bool e4m3, int splits, void* workspace, cudaStream_t st);
+size_t attend_few_bytes(int B, int Hkv, int d, long longest);
+cudaError_t launch_attend_few(const AttendArgs& a, bool e4m3, void* workspace, long longest, cudaStream_t st);
+// longest: tokens that a sequence's row of the page table has room for.
+size_t attend_workspace_bytes(int B, int H, int Hkv, long T, int d, long longest);
+cudaError_t launch_cache_attend(const AttendArgs& a, bool e4m3, void* workspace, long longest, cudaStream_t st);
 
 }  // namespace titans

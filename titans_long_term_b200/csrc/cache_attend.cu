@@ -695,33 +695,29 @@ int tile_splits(int B, int H, int Hkv, long T, long longest) {
 
 }  // namespace
 
-int attend_splits(int B, int H, int Hkv, long T, long longest) {
-    return attend_few_rows(H, Hkv, T) ? attend_few_splits(B, Hkv, longest) : tile_splits(B, H, Hkv, T, longest);
-}
-
-size_t attend_workspace_bytes(int B, int H, long T, int d, int splits) {
+size_t attend_workspace_bytes(int B, int H, int Hkv, long T, int d, long longest) {
+    if (attend_few_rows(H, Hkv, T)) return attend_few_bytes(B, Hkv, d, longest);
+    const int splits = tile_splits(B, H, Hkv, T, longest);
     return splits == 1 ? 0 : (size_t)splits * B * H * T * (d * sizeof(float) + sizeof(float2));
 }
 
-cudaError_t launch_cache_attend(const AttendArgs& args, bool e4m3, int splits, void* workspace, cudaStream_t st) {
+cudaError_t launch_cache_attend(const AttendArgs& args, bool e4m3, void* workspace, long longest, cudaStream_t st) {
+    if (attend_few_rows(args.c.H, args.c.Hkv, args.c.T)) return launch_attend_few(args, e4m3, workspace, longest, st);
     AttendArgs a = args;
+    const int splits = tile_splits(a.c.B, a.c.H, a.c.Hkv, a.c.T, longest);
     const size_t n = (size_t)splits * a.c.B * a.c.H * a.c.T;
     a.part = static_cast<float*>(workspace);
     a.part_ml = reinterpret_cast<float2*>(a.part + (splits > 1 ? n * a.c.d : 0));
+    // Two tiles of rows a CTA where that still leaves a CTA for most SMs
+    const long rows = a.c.T * (a.c.H / a.c.Hkv);
+    const bool two = rows > kRows && (rows + 2 * kRows - 1) / (2 * kRows) * a.c.B * a.c.Hkv * splits >= 100;
     cudaError_t e;
-    if (attend_few_rows(a.c.H, a.c.Hkv, a.c.T)) {
-        e = launch_attend_few(a, e4m3, splits, st);
+    if (a.c.d == 64) {
+        e = e4m3 ? (two ? launch<64, true, 2>(a, splits, st) : launch<64, true, 1>(a, splits, st))
+                 : (two ? launch<64, false, 2>(a, splits, st) : launch<64, false, 1>(a, splits, st));
     } else {
-        // Two tiles of rows a CTA where that still leaves a CTA for most SMs
-        const long rows = a.c.T * (a.c.H / a.c.Hkv);
-        const bool two = rows > kRows && (rows + 2 * kRows - 1) / (2 * kRows) * a.c.B * a.c.Hkv * splits >= 100;
-        if (a.c.d == 64) {
-            e = e4m3 ? (two ? launch<64, true, 2>(a, splits, st) : launch<64, true, 1>(a, splits, st))
-                     : (two ? launch<64, false, 2>(a, splits, st) : launch<64, false, 1>(a, splits, st));
-        } else {
-            e = e4m3 ? (two ? launch<128, true, 2>(a, splits, st) : launch<128, true, 1>(a, splits, st))
-                     : (two ? launch<128, false, 2>(a, splits, st) : launch<128, false, 1>(a, splits, st));
-        }
+        e = e4m3 ? (two ? launch<128, true, 2>(a, splits, st) : launch<128, true, 1>(a, splits, st))
+                 : (two ? launch<128, false, 2>(a, splits, st) : launch<128, false, 1>(a, splits, st));
     }
     if (e != cudaSuccess || splits == 1) return e;
     auto* kernel = a.c.d == 64 ? combine_kernel<64> : combine_kernel<128>;

@@ -1,16 +1,27 @@
 // Attention over the paged cache for up to sixteen rows of a key/value head (rows: its new tokens times the query heads
 // that share it), which reading the cache bounds: a decode step.
 //
-// Eight warps of a CTA take blocks of keys in turn, each with a maximum, sum and output of its own, joined in
-// shared memory at the end (and over the CTAs that split a sequence by combine_kernel). Nothing is staged: a lane loads
-// 16 consecutive bytes of a key or value row from the cache straight into the fragment of an m16n8k16 product.
-//   S = Q K^T: the sum over d may run in any order that Q and K share, so lane % 4 takes every fourth 16-byte
-//              piece of a row, in two (bf16) or four (e4m3) steps of 16 of d, and Q is loaded the same way.
-//   O += P V:  column n of an output tile may stand for any d, so lane / 4 takes a piece of consecutive d and its
-//              i-th value belongs to tile i; the values of two keys are paired by a byte permutation.
-// While one block is multiplied the next one's keys and values are on their way: 8 KiB a warp, 64 KiB an SM.
-// An e4m3 cache is converted to bf16 in registers, exactly; its scales multiply the scores and the weights.
-// A page holds at least 16 tokens, so 16 keys need one look into the page table.
+// One round of CTAs shares out all blocks of keys of all sequences evenly: CTA i of n takes blocks i total / n .. of the
+// sequence of (sequence, head, block), whatever the lengths are, so it may end one head's keys, go through
+// some more and begin another's. What is only a part of a head's keys goes to the workspace, two places a CTA
+// (the part its range begins with, and the part it ends with), and join_kernel adds the parts up.
+//
+// The warps of a CTA take blocks of keys in turn, each with a maximum, sum and output of its own, joined in
+// shared memory at the end of a head's keys. Nothing is staged: a lane loads 16 consecutive bytes of a key or value row
+// from the cache straight into the A fragment of m16n8k16 products, whose eight columns are the rows of Q.
+//   S^T = K Q^T:    the sum over d may run in any order that Q and K share, so lane % 4 takes every fourth 16-byte
+//                   piece of a row, in two (bf16) or four (e4m3) steps of 16 of d, and Q is loaded the same way.
+//   O^T += V^T P^T: row m of an output tile may stand for any d, so lane / 4 takes a piece of consecutive d, whose values
+//                   2 i and 2 i + 1 belong to tile i; the values of two keys are paired by a byte permutation.
+// With keys and values as the 16-row side, eight rows of Q (one token of up to eight heads) cost half the registers and
+// instructions of the other way round, and instructions, not bytes, bound that: 12 or 16 warps fit an SM.
+// While one block is multiplied the next one's keys and values are on their way, 64 KiB an SM or more.
+// A page holds at least 16 tokens, so 16 keys need one look into the page table, two blocks ahead of their use.
+//
+// An e4m3 cache is multiplied in fp16, to which one instruction converts two values exactly. Q goes to fp16
+// times a power of two of its row (largest element at 2^14..2^15: exact down to 2^-28 of it). Weights go to
+// fp16 as 2^(z + log2 s - M), s the scale of the key's values and M the running maximum of z + log2 s, so that the largest
+// contribution is near 1 whatever the scales are; their sum takes them back by 1 / s, in fp32.
 #include <algorithm>
 
 #include "cache_attend.cuh"
@@ -19,7 +30,7 @@
 namespace titans {
 namespace {
 
-constexpr int kWarps = 8, kM = 16;
+constexpr int kM = 16;
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -27,211 +38,306 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// Two e4m3 values as bf16, exactly.
-__device__ __forceinline__ uint32_t bf16_of(uint32_t e4m3x2) {
-    const float2 f = e4m3x2_to_float2((uint16_t)e4m3x2);
-    return pack_bf16x2(f.x, f.y);
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two e4m3 values as fp16, exactly.
+__device__ __forceinline__ uint32_t half_of(uint32_t e4m3x2) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((uint16_t)e4m3x2, __NV_E4M3);
+    return h.x | (uint32_t)h.y << 16;
 }
 
-template <int D, bool E4M3>
-__global__ void __launch_bounds__(kWarps * 32, 1) attend_few_kernel(AttendArgs a) {
-    constexpr int SUB = E4M3 ? 2 : 1, KEYS = 16 * SUB;  // a block: one or two times 16 keys
-    constexpr int KP = D * (E4M3 ? 1 : 2) / 64;         // 16-byte pieces of a key row for each of four lanes
-    constexpr int KW = E4M3 ? 8 : 4;                    // bf16 pairs of such a piece
-    constexpr int VE = E4M3 && D == 128 ? 16 : 8;       // consecutive values of a value row a lane takes,
-    constexpr int VG = D / 8 / VE;                      // in so many groups of 8 VE
-    constexpr int VB = VE * (E4M3 ? 1 : 2);             // bytes: 16, or 8 (e4m3, d = 64)
-    extern __shared__ __align__(16) float smem[];  // outputs [warps][16][D], then maxima and sums [warps][16]
+template <bool E4M3>
+constexpr int kBlock = 16;  // keys of a block
+
+// Blocks of keys of sequence b that its rows see.
+template <int KEYS>
+__device__ __forceinline__ Tiles blocks_of(const AttendArgs& a, int b) {
+    const int G = a.c.H / a.c.Hkv, n = min((int)a.c.T * G, cache_count(a.c, b) * G);
+    if (n <= 0) return Tiles{0, 0, 0};
+    const long start = a.c.starts[b];
+    return tiles_of<KEYS>(a, start, start + (n - 1) / G);
+}
+// The CTA of n whose share of `total` holds block x.
+__device__ __forceinline__ int owner(long x, long n, long total) { return (int)(((x + 1) * n - 1) / total); }
+
+// The 8 x 8 matrix of 16-bit values whose row lane / 4 the lanes hold in pairs, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// NQ: tiles of eight rows.
+template <int D, bool E4M3, int NQ>
+struct Few {
+    static constexpr int kKeys = kBlock<E4M3>, kSub = kKeys / 16;  // keys of a block, in sixteens
+    static constexpr int kWarps = NQ == 2 ? 8 : E4M3 ? 16 : 12;
+    static constexpr int kRows = 8 * NQ;
+    static constexpr int kBytes = kWarps * kRows * (D * (int)sizeof(float) + (int)sizeof(float2));
+    static constexpr int kKP = D * (E4M3 ? 1 : 2) / 64;  // 16-byte pieces of a key row for each of four lanes
+    static constexpr int kKW = E4M3 ? 8 : 4;             // pairs of values of such a piece
+    static constexpr int kVE = E4M3 && D == 128 ? 16 : 8;  // consecutive values of a value row a lane takes,
+    static constexpr int kVG = D / 8 / kVE;                // in so many groups of 8 kVE
+};
+
+// Keys first..last-1 (in blocks) of key/value head hk of sequence b: writes the rows' outputs, or, where that is a part of the
+// keys, their place in the workspace.
+template <int D, bool E4M3, int NQ>
+__device__ __forceinline__ void attend_head(const AttendArgs& a, int b, int hk, Tiles tiles, int first, int last, long place,
+                                            float* smem) {
+    using F = Few<D, E4M3, NQ>;
+    constexpr int SUB = F::kSub, KEYS = F::kKeys, KP = F::kKP, KW = F::kKW, VE = F::kVE, VG = F::kVG, W = F::kWarps;
+    constexpr int VB = VE * (E4M3 ? 1 : 2);  // bytes: 16, or 8 (e4m3, d = 64)
     const CacheArgs& c = a.c;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, q4 = lane & 3;
-    const int units = c.B * c.Hkv, unit = blockIdx.x % units, b = unit / c.Hkv, hk = unit % c.Hkv, G = c.H / c.Hkv;
-    const int rows = (int)c.T * G, count = cache_count(c, b);
+    const int G = c.H / c.Hkv, rows = (int)c.T * G, seen_rows = min(rows, cache_count(c, b) * G);
     const long start = c.starts[b];
-    const int seen_rows = min(rows, count * G), split = blockIdx.x / units, splits = gridDim.x / units;
-    Tiles tiles{0, 0, 0};
-    long see_lo = 0, see_hi = -1, sink_hi = 0;  // keys that some row sees: see_lo..see_hi, and below sink_hi
-    if (seen_rows > 0) {
-        see_hi = start + (seen_rows - 1) / G;
-        tiles = tiles_of<KEYS>(a, start, see_hi);
-        see_lo = seen_by(a, start).begin, sink_hi = seen_by(a, see_hi).sink_end;
-    }
-    const int first = (int)((long)tiles.count * split / splits), last = (int)((long)tiles.count * (split + 1) / splits);
+    const long see_hi = start + (seen_rows - 1) / G;  // keys that some row sees: see_lo..see_hi, and below sink_hi
+    const long see_lo = seen_by(a, start).begin, sink_hi = seen_by(a, see_hi).sink_end;
 
-    // This lane's rows r and r + 8
-    long p[2];
-    Seen seen[2];
-    bool live[2];
-    uint32_t q[KP * KW / 2][4];
-    const float scale = a.scale * 1.44269504f;
+    // Q's rows 8 n + r as B fragments
+    uint32_t q[NQ][KP * KW / 2][2];
+    float q_inv[NQ];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int row = r + 8 * h;
-        live[h] = row < seen_rows;
-        p[h] = start + row / G;
-        seen[h] = seen_by(a, p[h]);
+    for (int n = 0; n < NQ; ++n) {
+        const int row = 8 * n + r;
         const long at = (((long)b * c.H + hk * G + row % G) * c.T + row / G) * D;
 #pragma unroll
         for (int i = 0; i < KP; ++i)
 #pragma unroll
             for (int w = 0; w < KW; w += 2) {
                 uint2 u = make_uint2(0, 0);
-                if (live[h])
+                if (row < seen_rows)
                     u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.q) + at + (q4 + 4 * i) * 2 * KW +
                                                         2 * w);
-                q[(i * KW + w) / 2][h] = u.x, q[(i * KW + w) / 2][2 + h] = u.y;
+                q[n][(i * KW + w) / 2][0] = u.x, q[n][(i * KW + w) / 2][1] = u.y;
             }
+        q_inv[n] = 1.f;
+        if constexpr (E4M3) {
+            float top = 0.f;
+#pragma unroll
+            for (int i = 0; i < KP * KW; ++i) {
+                const float2 f = unpack_bf16x2(q[n][i >> 1][i & 1]);
+                top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int e = max(__float_as_int(top) >> 23, 27) - 127;
+            const float up = __int_as_float((14 - e + 127) << 23);
+            q_inv[n] = __int_as_float((e - 14 + 127) << 23);
+#pragma unroll
+            for (int i = 0; i < KP * KW; ++i) {
+                const float2 f = unpack_bf16x2(q[n][i >> 1][i & 1]);
+                const __half2 v = __floats2half2_rn(f.x * up, f.y * up);
+                q[n][i >> 1][i & 1] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+        }
     }
-    // Row of the pool where 16 keys from key0 on begin, or -1
-    auto find = [&](long key0) -> long {
-        if (key0 > see_hi || (key0 + 15 < see_lo && key0 >= sink_hi)) return -1;
-        const long at = cache_row(c, b, hk, key0);
-        if (at < 0 && lane == 0) atomicOr(c.status, kStatusMissingPage);
-        return at;
+    // Rows 8 n + 2 q4 + {0, 1}, whose scores this lane has (keys r and r + 8)
+    float scale[NQ][2], m[NQ][2], l[NQ][2] = {};
+#pragma unroll
+    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            scale[n][h] = a.scale * 1.44269504f * __shfl_sync(0xffffffffu, q_inv[n], (2 * q4 + h) * 4);
+            m[n][h] = -INFINITY;
+        }
+
+    // The page of 16 keys from key0 on: -2 where no row sees any of them, -1 where the table has none. Only the load, so
+    // that nothing waits for it until row_of.
+    auto page_of = [&](long key0) -> int {
+        if (key0 > see_hi || (key0 + 15 < see_lo && key0 >= sink_hi)) return -2;
+        const long index = key0 >> c.page_shift;
+        return index < c.max_pages ? max(c.table[(long)b * c.max_pages + index], -1) : -1;
+    };
+    // Row of the pool where they begin, or -1.
+    auto row_of = [&](int page, long key0) -> long {
+        if ((unsigned)page >= (unsigned)c.num_pages) {
+            if (page != -2 && lane == 0) atomicOr(c.status, kStatusMissingPage);
+            return -1;
+        }
+        return (((long)page * c.Hkv + hk) << c.page_shift) + (key0 & ((1 << c.page_shift) - 1));
     };
     uint4 kb[SUB][2][KP];
     uint4 vb[SUB][4][VG];
-    float ks[SUB][4], vs[SUB][4];  // e4m3: scales of the keys 2 q4 + {0, 1, 8, 9}
+    float ks[SUB][2], vs[SUB][2];  // e4m3: scales of the keys r and r + 8
     auto load_k = [&](const long (&at)[SUB]) {
 #pragma unroll
         for (int s = 0; s < SUB; ++s)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < 2; ++h) {
+                const uint4* src = static_cast<const uint4*>(c.pk) + (at[s] + r + 8 * h) * (4 * KP) + q4;
 #pragma unroll
-                for (int i = 0; i < KP; ++i) {
-                    kb[s][h][i] = make_uint4(0, 0, 0, 0);
-                    if (at[s] >= 0)
-                        kb[s][h][i] = static_cast<const uint4*>(c.pk)[(at[s] + r + 8 * h) * (4 * KP) + q4 + 4 * i];
-                }
-        if constexpr (E4M3) {
-#pragma unroll
-            for (int s = 0; s < SUB; ++s)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) ks[s][e] = at[s] >= 0 ? c.k_scale[at[s] + 2 * q4 + (e & 1) + (e >> 1) * 8] : 0.f;
-        }
+                for (int i = 0; i < KP; ++i) kb[s][h][i] = at[s] >= 0 ? src[4 * i] : make_uint4(0, 0, 0, 0);
+                if constexpr (E4M3) ks[s][h] = at[s] >= 0 ? c.k_scale[at[s] + r + 8 * h] : 0.f;
+            }
     };
     // Values that no row sees are zeros: their weights are 0, and 0 times an infinity or NaN would not be.
     auto load_v = [&](const long (&at)[SUB], long key0) {
+        const bool all = key0 + KEYS - 1 <= see_hi && (key0 >= see_lo || key0 + KEYS <= sink_hi);
 #pragma unroll
-        for (int s = 0; s < SUB; ++s)
+        for (int s = 0; s < SUB; ++s) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int k = 2 * q4 + (e & 1) + (e >> 1) * 8;
-                const long key = key0 + 16 * s + k;
-                const bool there = at[s] >= 0 && key <= see_hi && (key >= see_lo || key < sink_hi);
+                bool there = at[s] >= 0;
+                if (!all) {
+                    const long key = key0 + 16 * s + k;
+                    there = there && key <= see_hi && (key >= see_lo || key < sink_hi);
+                }
+                const char* src = static_cast<const char*>(c.pv) + (at[s] + k) * (D * (E4M3 ? 1 : 2)) + r * VB;
 #pragma unroll
                 for (int g = 0; g < VG; ++g) {
                     vb[s][e][g] = make_uint4(0, 0, 0, 0);
-                    const char* src = static_cast<const char*>(c.pv) + (at[s] + k) * (D * (E4M3 ? 1 : 2)) + (g * 8 + r) * VB;
                     if (there) {
                         if constexpr (VB == 16) {
-                            vb[s][e][g] = *reinterpret_cast<const uint4*>(src);
+                            vb[s][e][g] = *reinterpret_cast<const uint4*>(src + g * 8 * VB);
                         } else {
-                            const uint2 u = *reinterpret_cast<const uint2*>(src);
+                            const uint2 u = *reinterpret_cast<const uint2*>(src + g * 8 * VB);
                             vb[s][e][g].x = u.x, vb[s][e][g].y = u.y;
                         }
                     }
                 }
-                if constexpr (E4M3) vs[s][e] = there ? c.v_scale[at[s] + k] : 0.f;
             }
+            if constexpr (E4M3)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) vs[s][h] = at[s] >= 0 ? c.v_scale[at[s] + r + 8 * h] : 0.f;
+        }
     };
 
-    float o[VG][VE][4] = {}, m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float o[VG][VE / 2][NQ][4] = {};
     long at[SUB], at_next[SUB];
-    auto find_all = [&](int i, long (&x)[SUB]) {
+    int page[SUB];  // of the block after the next one
+    auto pages_of = [&](int i) {
 #pragma unroll
-        for (int s = 0; s < SUB; ++s) x[s] = i < last ? find((long)tiles[i] * KEYS + 16 * s) : -1;
+        for (int s = 0; s < SUB; ++s) page[s] = i < last ? page_of((long)tiles[i] * KEYS + 16 * s) : -2;
+    };
+    auto rows_of = [&](int i, long(&x)[SUB]) {
+#pragma unroll
+        for (int s = 0; s < SUB; ++s) x[s] = row_of(page[s], (long)tiles[i] * KEYS + 16 * s);
     };
     int i = first + warp;
-    find_all(i, at);
+    pages_of(i);
+    rows_of(i, at);
+    pages_of(i + W);
     load_k(at);
-    load_v(at, i < last ? (long)tiles[i] * KEYS : 0);
-    find_all(i + kWarps, at_next);
-    for (; i < last; i += kWarps) {
+    load_v(at, (long)tiles[i] * KEYS);
+    for (; i < last; i += W) {
         const long key0 = (long)tiles[i] * KEYS;
-        float sc[2 * SUB][4] = {};
+        rows_of(i + W, at_next);
+        pages_of(i + 2 * W);
+        float sc[SUB][NQ][4] = {};
 #pragma unroll
         for (int s = 0; s < SUB; ++s)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)  // keys 8 h .. of the sixteen
+            for (int j = 0; j < KP; ++j) {
+                const uint32_t x[4] = {kb[s][0][j].x, kb[s][0][j].y, kb[s][0][j].z, kb[s][0][j].w};
+                const uint32_t y[4] = {kb[s][1][j].x, kb[s][1][j].y, kb[s][1][j].z, kb[s][1][j].w};
 #pragma unroll
-                for (int j = 0; j < KP; ++j) {
-                    const uint4 u = kb[s][h][j];
-                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                for (int t = 0; t < KW / 2; ++t) {
+                    uint32_t f[4];
                     if constexpr (E4M3) {
-#pragma unroll
-                        for (int t = 0; t < 4; ++t)
-                            mma_bf16(sc[2 * s + h], q[j * 4 + t], bf16_of(w[t]), bf16_of(w[t] >> 16));
+                        f[0] = half_of(x[t]), f[1] = half_of(y[t]), f[2] = half_of(x[t] >> 16), f[3] = half_of(y[t] >> 16);
                     } else {
-                        mma_bf16(sc[2 * s + h], q[j * 2], w[0], w[1]);
-                        mma_bf16(sc[2 * s + h], q[j * 2 + 1], w[2], w[3]);
+                        f[0] = x[2 * t], f[1] = y[2 * t], f[2] = x[2 * t + 1], f[3] = y[2 * t + 1];
+                    }
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) {
+                        const uint32_t(&u)[2] = q[n][j * KW / 2 + t];
+                        if constexpr (E4M3)
+                            mma_f16(sc[s][n], f, u[0], u[1]);
+                        else
+                            mma_bf16(sc[s][n], f, u[0], u[1]);
                     }
                 }
-        float kscale[SUB][4];
-        bool there[SUB];
-#pragma unroll
-        for (int s = 0; s < SUB; ++s) {
-            there[s] = at[s] >= 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) kscale[s][e] = E4M3 ? ks[s][e] * scale : scale;
-        }
-        load_k(at_next);
-        // Scores in log2 units; -infinity where the row does not see the key
-        bool whole = true;
-#pragma unroll
-        for (int s = 0; s < SUB; ++s) whole = whole && there[s];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) whole = whole && (!live[h] || (key0 >= seen[h].begin && key0 + KEYS - 1 <= p[h]));
-        whole = __all_sync(0xffffffffu, whole);
-        float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-        for (int t = 0; t < 2 * SUB; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int h = e >> 1;
-                float x = sc[t][e] * kscale[t >> 1][(t & 1) * 2 + (e & 1)];
-                if (!whole) {
-                    const long key = key0 + 8 * t + 2 * q4 + (e & 1);
-                    if (!there[t >> 1] || key > p[h] || (key < seen[h].begin && key >= seen[h].sink_end)) x = -INFINITY;
-                }
-                sc[t][e] = x;
-                top[h] = fmaxf(top[h], x);
             }
+        // Scores in log2 units (e4m3: plus that of the value's scale); -infinity where the row does not see the key
+        bool whole = key0 >= seen_by(a, see_hi).begin && key0 + KEYS - 1 <= start;
+#pragma unroll
+        for (int s = 0; s < SUB; ++s) whole = whole && at[s] >= 0;
+        float inv[SUB][2], top[NQ][2];
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) top[n][0] = top[n][1] = -INFINITY;
+#pragma unroll
+        for (int s = 0; s < SUB; ++s)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {  // keys r, r + 8
+                float k_scale = 1.f, v_log = 0.f;
+                if constexpr (E4M3) {
+                    k_scale = ks[s][e], v_log = lg2(vs[s][e]);
+                    inv[s][e] = vs[s][e] > 0.f ? __fdividef(1.f, vs[s][e]) : 0.f;
+                }
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float& x = sc[s][n][2 * e + h];
+                        x = fmaf(x, k_scale * scale[n][h], v_log);
+                        if (!whole) {
+                            const long key = key0 + 16 * s + 8 * e + r, p = start + (8 * n + 2 * q4 + h) / G;
+                            const Seen v = seen_by(a, p);
+                            if (at[s] < 0 || key > p || (key < v.begin && key >= v.sink_end)) x = -INFINITY;
+                        }
+                        top[n][h] = fmaxf(top[n][h], x);
+                    }
+            }
+        load_k(at_next);
         bool grown = false;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
-            top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
-            grown = grown || top[h] - m[h] > 8.f || (m[h] == -INFINITY && top[h] > m[h]);
-        }
-        if (__any_sync(0xffffffffu, grown)) {
+        for (int n = 0; n < NQ; ++n)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const float next = fmaxf(m[h], top[h]), keep = m[h] == next ? 1.f : ex2(m[h] - next);
-                m[h] = next;
-                l[h] *= keep;
 #pragma unroll
-                for (int g = 0; g < VG; ++g)
-#pragma unroll
-                    for (int e = 0; e < VE; ++e) o[g][e][2 * h] *= keep, o[g][e][2 * h + 1] *= keep;
+                for (int d = 4; d < 32; d <<= 1) top[n][h] = fmaxf(top[n][h], __shfl_xor_sync(0xffffffffu, top[n][h], d));
+                grown = grown || top[n][h] - m[n][h] > 8.f || (m[n][h] == -INFINITY && top[n][h] > m[n][h]);
             }
-        }
-        const float shift[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+        if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
-        for (int s = 0; s < SUB; ++s) {
-            uint32_t w[4];
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int n = 0; n < NQ; ++n)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    float x = ex2(sc[2 * s + t][2 * h] - shift[h]), y = ex2(sc[2 * s + t][2 * h + 1] - shift[h]);
-                    l[h] += x + y;
-                    if constexpr (E4M3) x *= vs[s][2 * t], y *= vs[s][2 * t + 1];  // powers of two: no rounding
-                    w[2 * t + h] = pack_bf16x2(x, y);
+                    const float next = fmaxf(m[n][h], top[n][h]), keep = m[n][h] == next ? 1.f : ex2(m[n][h] - next);
+                    m[n][h] = next;
+                    l[n][h] *= keep;
+#pragma unroll
+                    for (int g = 0; g < VG; ++g)
+#pragma unroll
+                        for (int e = 0; e < VE / 2; ++e) o[g][e][n][h] *= keep, o[g][e][n][2 + h] *= keep;
+                }
+        }
+#pragma unroll
+        for (int s = 0; s < SUB; ++s) {
+            uint32_t w[NQ][2];  // weights as B fragments
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float x[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        x[h] = ex2(sc[s][n][2 * e + h] - (m[n][h] == -INFINITY ? 0.f : m[n][h]));
+                        l[n][h] = E4M3 ? fmaf(x[h], inv[s][e], l[n][h]) : l[n][h] + x[h];
+                    }
+                    if constexpr (E4M3) {
+                        const __half2 v = __floats2half2_rn(x[0], x[1]);
+                        w[n][e] = transpose8(*reinterpret_cast<const uint32_t*>(&v));
+                    } else {
+                        w[n][e] = transpose8(pack_bf16x2(x[0], x[1]));
+                    }
                 }
 #pragma unroll
             for (int g = 0; g < VG; ++g) {
@@ -240,98 +346,215 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_few_kernel(AttendArgs a
                                           {vb[s][2][g].x, vb[s][2][g].y, vb[s][2][g].z, vb[s][2][g].w},
                                           {vb[s][3][g].x, vb[s][3][g].y, vb[s][3][g].z, vb[s][3][g].w}};
 #pragma unroll
-                for (int e = 0; e < VE; e += 2) {
-                    uint32_t x[4];  // values e, e + 1 of the four keys
+                for (int e = 0; e < VE / 2; ++e) {
+                    uint32_t x[4], f[4];  // values 2 e, 2 e + 1 of the four keys
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        x[k] = E4M3 ? bf16_of(v[k][e >> 2] >> (e & 2) * 8) : v[k][e >> 1];
-                    mma_bf16(o[g][e], w, __byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410));
-                    mma_bf16(o[g][e + 1], w, __byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x7632));
+                    for (int k = 0; k < 4; ++k) x[k] = E4M3 ? half_of(v[k][e >> 1] >> (e & 1) * 16) : v[k][e];
+                    f[0] = __byte_perm(x[0], x[1], 0x5410), f[1] = __byte_perm(x[0], x[1], 0x7632);
+                    f[2] = __byte_perm(x[2], x[3], 0x5410), f[3] = __byte_perm(x[2], x[3], 0x7632);
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) {
+                        if constexpr (E4M3)
+                            mma_f16(o[g][e][n], f, w[n][0], w[n][1]);
+                        else
+                            mma_bf16(o[g][e][n], f, w[n][0], w[n][1]);
+                    }
                 }
             }
         }
-        load_v(at_next, i + kWarps < last ? (long)tiles[i + kWarps] * KEYS : 0);
+        load_v(at_next, (long)tiles[i + W] * KEYS);
 #pragma unroll
         for (int s = 0; s < SUB; ++s) at[s] = at_next[s];
-        find_all(i + 2 * kWarps, at_next);
     }
 
-    // Join the warps: row by row, in the order of the warps
+    // Join the warps, row by row, in their order
     float* out = smem;
-    float2* ml = reinterpret_cast<float2*>(smem + kWarps * kM * D);
+    float2* ml = reinterpret_cast<float2*>(smem + W * F::kRows * D);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-        const int row = r + 8 * h;
-        if (q4 == 0) ml[warp * kM + row] = make_float2(m[h], l[h]);
+    for (int n = 0; n < NQ; ++n)
 #pragma unroll
-        for (int g = 0; g < VG; ++g)
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-            for (int n = 0; n < 2; ++n)  // column 2 q4 + n stands for d = 8 g VE + (2 q4 + n) VE + e
+            for (int d = 4; d < 32; d <<= 1) l[n][h] += __shfl_xor_sync(0xffffffffu, l[n][h], d);
+            const int row = warp * F::kRows + 8 * n + 2 * q4 + h;
+            if (r == 0) ml[row] = make_float2(m[n][h], l[n][h]);
 #pragma unroll
-                for (int e = 0; e < VE; ++e)
-                    out[(warp * kM + row) * D + g * 8 * VE + (2 * q4 + n) * VE + e] = o[g][e][2 * h + n];
-    }
+            for (int g = 0; g < VG; ++g)
+#pragma unroll
+                for (int e = 0; e < VE / 2; ++e)
+                    *reinterpret_cast<float2*>(out + row * D + (g * 8 + r) * VE + 2 * e) =
+                        make_float2(o[g][e][n][h], o[g][e][n][2 + h]);
+        }
     __syncthreads();
-    for (int row = warp; row < rows && row < kM; row += kWarps) {  // one warp a row, D / 32 columns a lane
+    const bool part = first > 0 || last < tiles.count;
+    for (int row = warp; row < rows; row += W) {  // one warp a row, D / 32 columns a lane
         constexpr int N = D / 32;
         const int t = row / G;
         const long orow = ((long)b * c.H + hk * G + row % G) * c.T + t;
         float top = -INFINITY, sum = 0.f, acc[N] = {};
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * kM + row].x);
-        for (int w = 0; w < kWarps; ++w) {
-            const float2 x = ml[w * kM + row];
+        for (int w = 0; w < W; ++w) top = fmaxf(top, ml[w * F::kRows + row].x);
+        for (int w = 0; w < W; ++w) {
+            const float2 x = ml[w * F::kRows + row];
             if (x.x == -INFINITY && x.y == 0.f) continue;
             const float f = x.x == top ? 1.f : ex2(x.x - top);
             sum = fmaf(x.y, f, sum);
 #pragma unroll
-            for (int i = 0; i < N; ++i) acc[i] = fmaf(out[(w * kM + row) * D + lane * N + i], f, acc[i]);
+            for (int j = 0; j < N; ++j) acc[j] = fmaf(out[(w * F::kRows + row) * D + lane * N + j], f, acc[j]);
         }
         bool fine = fabsf(sum) < INFINITY;
 #pragma unroll
-        for (int i = 0; i < N; ++i) fine = fine && fabsf(acc[i]) < INFINITY;
+        for (int j = 0; j < N; ++j) fine = fine && fabsf(acc[j]) < INFINITY;
         if (row < seen_rows && !__all_sync(0xffffffffu, fine))
             attend_row<D, E4M3, KEYS>(a, b, hk, static_cast<const __nv_bfloat16*>(a.q) + orow * D, start + t, tiles, first,
                                       last, top, sum, acc);
-        if (splits > 1) {
-            const long prow = (long)split * c.B * c.H * c.T + orow;
+        if (part) {
+            const long prow = place * kM + row;
 #pragma unroll
-            for (int i = 0; i < N; ++i) a.part[prow * D + lane * N + i] = acc[i];
+            for (int j = 0; j < N; ++j) a.part[prow * D + lane * N + j] = acc[j];
             if (lane == 0) a.part_ml[prow] = make_float2(top, sum);
         } else {
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const float inv = sum == 0.f || row >= seen_rows ? 0.f : 1.f / sum;
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                static_cast<__nv_bfloat16*>(a.o)[orow * D + lane * N + i] = __float2bfloat16(acc[i] * inv);
+            for (int j = 0; j < N; ++j)
+                static_cast<__nv_bfloat16*>(a.o)[orow * D + lane * N + j] = __float2bfloat16(inv == 0.f ? 0.f : acc[j] * inv);
         }
+    }
+    __syncthreads();  // the next head's outputs come into the same places
+}
+
+template <int D, bool E4M3, int NQ>
+__global__ void __launch_bounds__(Few<D, E4M3, NQ>::kWarps * 32, 1) attend_few_kernel(AttendArgs a) {
+    constexpr int W = Few<D, E4M3, NQ>::kWarps, KEYS = kBlock<E4M3>;
+    extern __shared__ __align__(16) float smem[];  // outputs [warps][rows][D], then maxima and sums [warps][rows]
+    __shared__ long warp_sums[W];
+    __shared__ long found[2];  // sequence where the share's first block lies, and where its blocks begin
+    const CacheArgs& c = a.c;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // The share: prefix sums over the sequences, first for the total, then for the share's begin
+    long total = 0;
+    for (int pass = 0; pass < 2; ++pass) {
+        long base = 0;
+        const long x0 = total * blockIdx.x / gridDim.x;
+        for (int b0 = 0; b0 < c.B; b0 += W * 32) {
+            const int b = b0 + threadIdx.x;
+            const long n = b < c.B ? (long)blocks_of<KEYS>(a, b).count * c.Hkv : 0;
+            long sum = n;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const long y = __shfl_up_sync(0xffffffffu, sum, d);
+                if (lane >= d) sum += y;
+            }
+            __syncthreads();
+            if (lane == 31) warp_sums[warp] = sum;
+            __syncthreads();
+            long begin = base + sum - n;
+            for (int w = 0; w < W; ++w) {
+                if (w < warp) begin += warp_sums[w];
+                base += warp_sums[w];
+            }
+            if (pass && x0 >= begin && x0 < begin + n) found[0] = b, found[1] = begin;
+            if (pass && blockIdx.x == 0 && b < c.B) a.begins[b] = begin;
+        }
+        if (pass && blockIdx.x == 0 && threadIdx.x == 0) a.begins[c.B] = total;
+        total = base;
+        if (total == 0) return;  // join_kernel writes the zeros
+    }
+    __syncthreads();
+    const long x_begin = total * blockIdx.x / gridDim.x, x_end = total * (blockIdx.x + 1) / gridDim.x;
+    if (x_begin == x_end) return;
+    int b = (int)found[0];
+    Tiles tiles = blocks_of<KEYS>(a, b);
+    int hk = (int)((x_begin - found[1]) / tiles.count), first = (int)((x_begin - found[1]) % tiles.count);
+    for (long x = x_begin; x < x_end;) {
+        while (tiles.count == 0 || hk == c.Hkv) hk = 0, tiles = blocks_of<KEYS>(a, ++b);
+        const int last = (int)min((long)tiles.count, first + x_end - x);
+        attend_head<D, E4M3, NQ>(a, b, hk, tiles, first, last, (long)blockIdx.x * 2 + (x > x_begin), smem);
+        x += last - first;
+        first = 0, ++hk;
     }
 }
 
-template <int D, bool E4M3>
-cudaError_t launch(const AttendArgs& a, int splits, cudaStream_t st) {
-    constexpr int bytes = kWarps * kM * (D * (int)sizeof(float) + (int)sizeof(float2));
-    auto* kernel = attend_few_kernel<D, E4M3>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+// The rows of the heads whose keys more than one CTA had, and of sequences without any: one warp a row.
+template <int D, int KEYS>
+__global__ void __launch_bounds__(128) join_kernel(AttendArgs a, int ctas) {
+    constexpr int N = D / 32;
+    const CacheArgs& c = a.c;
+    const int G = c.H / c.Hkv, rows = (int)c.T * G, lane = threadIdx.x & 31;
+    const long at = (long)blockIdx.x * 4 + (threadIdx.x >> 5), unit = at / rows;
+    if (unit >= (long)c.B * c.Hkv) return;
+    const int row = (int)(at % rows), b = (int)(unit / c.Hkv), hk = (int)(unit % c.Hkv);
+    const int n = blocks_of<KEYS>(a, b).count;
+    float top = -INFINITY, sum = 0.f, acc[N] = {};
+    if (n > 0) {
+        const long total = a.begins[c.B], x0 = a.begins[b] + (long)hk * n;
+        const int c0 = owner(x0, ctas, total), c1 = owner(x0 + n - 1, ctas, total);
+        if (c0 == c1) return;  // written already
+        bool nan = false;
+        auto idle = [&](int i) { return total * i / ctas == total * (i + 1) / ctas; };  // fewer blocks than CTAs
+        auto place = [&](int i) { return ((long)i * 2 + (i == c0 && x0 > total * i / ctas)) * kM + row; };
+        for (int i = c0; i <= c1; ++i) {
+            if (idle(i)) continue;
+            const float m = a.part_ml[place(i)].x;
+            top = fmaxf(top, m);
+            nan = nan || m != m;
+        }
+        for (int i = c0; i <= c1; ++i) {
+            if (idle(i)) continue;
+            const float2 ml = a.part_ml[place(i)];
+            if (ml.x == -INFINITY && ml.y == 0.f) continue;
+            const float f = nan ? NAN : ml.x == top ? 1.f : ex2(ml.x - top);
+            sum = fmaf(ml.y, f, sum);
+#pragma unroll
+            for (int j = 0; j < N; ++j) acc[j] = fmaf(a.part[place(i) * D + lane * N + j], f, acc[j]);
+        }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const long orow = ((long)b * c.H + hk * G + row % G) * c.T + row / G;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        static_cast<__nv_bfloat16*>(a.o)[orow * D + lane * N + j] = __float2bfloat16(acc[j] * inv);
+}
+
+template <int D, bool E4M3, int NQ>
+cudaError_t launch(const AttendArgs& a, int ctas, cudaStream_t st) {
+    using F = Few<D, E4M3, NQ>;
+    auto* kernel = attend_few_kernel<D, E4M3, NQ>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kBytes);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)((long)a.c.B * a.c.Hkv * splits), kWarps * 32, bytes, st>>>(a);
+    kernel<<<(unsigned)ctas, F::kWarps * 32, F::kBytes, st>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const long rows = (long)a.c.B * a.c.H * a.c.T;
+    join_kernel<D, F::kKeys><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(a, ctas);
     return cudaGetLastError();
+}
+template <int D, bool E4M3>
+cudaError_t launch(const AttendArgs& a, int ctas, cudaStream_t st) {
+    return a.c.T * (a.c.H / a.c.Hkv) <= 8 ? launch<D, E4M3, 1>(a, ctas, st) : launch<D, E4M3, 2>(a, ctas, st);
+}
+
+// One CTA an SM, and at least 16 blocks of the longest possible sequences each, two a warp.
+int ctas_for(int B, int Hkv, long longest) {
+    return (int)std::max(1L, std::min(148L, (longest / 16 * B * Hkv + 15) / 16));
 }
 
 }  // namespace
 
 bool attend_few_rows(int H, int Hkv, long T) { return T * (H / Hkv) <= kM; }
 
-// CTAs for about four rounds over the SMs, so that sequences of different lengths even out, and at least 16 blocks of the
-// longest possible sequence a CTA, two a warp.
-int attend_few_splits(int B, int Hkv, long longest) {
-    const long base = (long)B * Hkv;
-    return (int)std::max(1L, std::min({longest / (16 * 16), (4 * 148L + base - 1) / base, 64L}));
+size_t attend_few_bytes(int B, int Hkv, int d, long longest) {
+    const size_t places = (size_t)ctas_for(B, Hkv, longest) * 2 * kM;
+    return places * (d * sizeof(float) + sizeof(float2)) + ((size_t)B + 1) * sizeof(long);
 }
 
-cudaError_t launch_attend_few(const AttendArgs& a, bool e4m3, int splits, cudaStream_t st) {
-    if (a.c.d == 64) return e4m3 ? launch<64, true>(a, splits, st) : launch<64, false>(a, splits, st);
-    return e4m3 ? launch<128, true>(a, splits, st) : launch<128, false>(a, splits, st);
+cudaError_t launch_attend_few(const AttendArgs& args, bool e4m3, void* workspace, long longest, cudaStream_t st) {
+    AttendArgs a = args;
+    const int ctas = ctas_for(a.c.B, a.c.Hkv, longest);
+    const size_t places = (size_t)ctas * 2 * kM;
+    a.part = static_cast<float*>(workspace);
+    a.part_ml = reinterpret_cast<float2*>(a.part + places * a.c.d);
+    a.begins = reinterpret_cast<long*>(a.part_ml + places);
+    if (a.c.d == 64) return e4m3 ? launch<64, true>(a, ctas, st) : launch<64, false>(a, ctas, st);
+    return e4m3 ? launch<128, true>(a, ctas, st) : launch<128, false>(a, ctas, st);
 }
 
 }  // namespace titans
