@@ -240,3 +240,22 @@ def test_binding_refuses_tensors():
         assert e.value.status == mem.EINVAL
     with pytest.raises(TitansError):
         p.cache.read(p.pages, p.table, starts, 0)
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_positions_behind_the_table(T):
+    """Queries that stand behind the table's last position see what it has room for, and that is recorded."""
+    p = Pool(2, 4, 2, 64, "bf16", 32, 320, seed=T)
+    q = p.q(T)
+    o = p.cache.attend(q, p.pages, p.table, ints(310, (1 << 31) - 1))
+    with pytest.raises(TitansError):
+        p.cache.sync_status()
+    k, v = (torch.cat([x, x.new_zeros(2, 2, 70, 64)], 2) for x in (p.k, p.v))
+    missing = torch.zeros(2, 390, dtype=torch.bool, device="cuda")
+    missing[:, 320:] = True
+    want = cache_ref.attend(q, k, v, [310, 350], [T, T], missing=missing)
+    assert ((o.double() - want).abs() / cache_ref.bar(want, p.v)).max() <= 1
+    o = p.cache.attend(q, p.pages, p.table, ints((1 << 31) - 1, 0), window=50)
+    with pytest.raises(TitansError):
+        p.cache.sync_status()
+    assert (o[0] == 0).all() and (o[1] != 0).any()

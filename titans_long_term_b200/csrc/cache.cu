@@ -52,14 +52,13 @@ __device__ __forceinline__ uint2 quantise(uint4 u, float& scale) {
     return r;
 }
 
-__device__ __forceinline__ uint32_t bf16x2_scaled(uint16_t e4m3x2, float scale) {
-    const float2 f = e4m3x2_to_float2(e4m3x2);
+__device__ __forceinline__ uint32_t bf16x2_scaled(float2 f, float scale) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(f.x * scale, f.y * scale);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 __device__ __forceinline__ uint4 dequantise(uint2 u, float scale) {
-    return make_uint4(bf16x2_scaled((uint16_t)u.x, scale), bf16x2_scaled((uint16_t)(u.x >> 16), scale),
-                      bf16x2_scaled((uint16_t)u.y, scale), bf16x2_scaled((uint16_t)(u.y >> 16), scale));
+    return make_uint4(bf16x2_scaled(e4m3_to_float2<false>(u.x), scale), bf16x2_scaled(e4m3_to_float2<true>(u.x), scale),
+                      bf16x2_scaled(e4m3_to_float2<false>(u.y), scale), bf16x2_scaled(e4m3_to_float2<true>(u.y), scale));
 }
 
 template <int D, bool E4M3>

@@ -36,9 +36,19 @@ __device__ __forceinline__ long cache_row(const CacheArgs& a, int b, int h, long
     return (((long)page * a.Hkv + h) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
 }
 
-// Two e4m3 values, exactly.
-__device__ __forceinline__ float2 e4m3x2_to_float2(uint16_t u) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(u, __NV_E4M3);
+// The lower (UPPER: upper) two of four e4m3 values as fp16, exactly.
+template <bool UPPER>
+__device__ __forceinline__ uint32_t e4m3_to_half2(uint32_t four) {
+    uint32_t y;
+    if constexpr (UPPER)
+        asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n cvt.rn.f16x2.e4m3x2 %0, hi;\n}" : "=r"(y) : "r"(four));
+    else
+        asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n}" : "=r"(y) : "r"(four));
+    return y;
+}
+template <bool UPPER>
+__device__ __forceinline__ float2 e4m3_to_float2(uint32_t four) {
+    const uint32_t h = e4m3_to_half2<UPPER>(four);
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 

@@ -83,15 +83,15 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
 
 // Eight e4m3 values times their scale as bf16: both steps exact.
 __device__ __forceinline__ uint4 to_bf16(uint32_t lo, uint32_t hi, float s) {
-    const float2 a = e4m3x2_to_float2((uint16_t)lo), b = e4m3x2_to_float2((uint16_t)(lo >> 16));
-    const float2 c = e4m3x2_to_float2((uint16_t)hi), d = e4m3x2_to_float2((uint16_t)(hi >> 16));
+    const float2 a = e4m3_to_float2<false>(lo), b = e4m3_to_float2<true>(lo);
+    const float2 c = e4m3_to_float2<false>(hi), d = e4m3_to_float2<true>(hi);
     return make_uint4(pack_bf16x2(a.x * s, a.y * s), pack_bf16x2(b.x * s, b.y * s), pack_bf16x2(c.x * s, c.y * s),
                       pack_bf16x2(d.x * s, d.y * s));
 }
 
-// Bits of the 32 keys from k0 on that lie in lo..hi.
-__device__ __forceinline__ uint32_t range_mask(long k0, long lo, long hi) {
-    const int a = (int)max(0L, min(32L, lo - k0)), e = (int)max(0L, min(32L, hi + 1 - k0));
+// Bits of the 32 keys from k0 on that lie in lo..end-1.
+__device__ __forceinline__ uint32_t range_mask(int k0, int lo, int end) {
+    const int a = max(0, min(32, lo - k0)), e = max(0, min(32, end - k0));
     const uint32_t below_a = a == 32 ? 0xffffffffu : (1u << a) - 1, below_e = e == 32 ? 0xffffffffu : (1u << e) - 1;
     return below_e & ~below_a;
 }
@@ -154,7 +154,12 @@ __global__ void __launch_bounds__(Plan<E4M3, NT>::kThreads, 1)
     const long start = c.starts[b];
     const long t_lo = row0 / G, t_hi = min(min(row0 + NT * kRows, rows) - 1, (long)count * G - 1) / G;
     Tiles tiles{0, 0, 0};
-    if (row0 < (long)count * G) tiles = tiles_of<kKeys>(a, start + t_lo, start + t_hi);
+    Seen seen_any{0, 0, 0};  // keys that some row of the CTA sees
+    if (row0 < (long)count * G) {
+        seen_any = seen_by_any(a, start + t_lo, start + t_hi);
+        tiles = tiles_of<kKeys>(seen_any);
+        if (tid == 0 && start + t_hi >= capacity(c)) atomicOr(c.status, kStatusMissingPage);
+    }
     const int first = (int)((long)tiles.count * blockIdx.z / gridDim.z);
     const int last = (int)((long)tiles.count * (blockIdx.z + 1) / gridDim.z), n = last - first;
 
@@ -245,8 +250,8 @@ __global__ void __launch_bounds__(Plan<E4M3, NT>::kThreads, 1)
             uint32_t x[2][32];
             tmem_ld32(ts, x[0]);
             tmem_ld32(ts + 32, x[1]);
-            const long k0 = (long)tiles[first + j] * kKeys;
-            const bool whole = k0 >= seen.begin && k0 + kKeys - 1 <= p &&
+            const int k0 = tiles[first + j] * kKeys;
+            const bool whole = k0 >= seen.begin && k0 + kKeys <= seen.end &&
                                (s.valid[stage][0] & s.valid[stage][1] & s.valid[stage][2] & s.valid[stage][3]) == ~0u;
             const bool all_whole = __all_sync(0xffffffffu, whole || !live);
             uint32_t mask[kChunks];
@@ -254,8 +259,8 @@ __global__ void __launch_bounds__(Plan<E4M3, NT>::kThreads, 1)
             for (int i = 0; i < kChunks; ++i) {
                 mask[i] = ~0u;
                 if (!all_whole) {
-                    const long kc = k0 + 32 * (i + 2 * half);
-                    mask[i] = (range_mask(kc, seen.begin, p) | range_mask(kc, 0, seen.sink_end - 1)) & s.valid[stage][i + 2 * half];
+                    const int kc = k0 + 32 * (i + 2 * half);
+                    mask[i] = (range_mask(kc, seen.begin, seen.end) | range_mask(kc, 0, min(seen.sink_end, seen.end))) & s.valid[stage][i + 2 * half];
                 }
             }
             auto masked = [&](uint32_t(&v)[32], uint32_t bits) {  // -infinity where the row does not see the key
@@ -413,9 +418,6 @@ __global__ void __launch_bounds__(Plan<E4M3, NT>::kThreads, 1)
     } else if (E4M3 ? warp >= kProducer0 : warp == kProducer0) {  // ------------- producers
         if constexpr (P::kSoftmaxRegs > 0) registers_down<E4M3 ? P::kProducerRegs : P::kIssueRegs>();
         // keys that no row of the CTA sees are neither looked up nor read
-        const long see_hi = start + t_hi;
-        const Seen lo = seen_by(a, start + t_lo), hi = seen_by(a, see_hi);
-        auto needed = [&](long key) { return key <= see_hi && (key >= lo.begin || key < hi.sink_end); };
         bool ok = true;
         if constexpr (!E4M3) {  // one warp
             int raw_uses[STAGES] = {}, last_parity[STAGES];
@@ -423,13 +425,13 @@ __global__ void __launch_bounds__(Plan<E4M3, NT>::kThreads, 1)
             const int page = 1 << c.page_shift, per_tile = kKeys >> c.page_shift;
             for (int j = 0; j < n && ok; ++j) {
                 const int stage = j % STAGES;
-                const long k0 = (long)tiles[first + j] * kKeys;
+                const int k0 = tiles[first + j] * kKeys;
                 // one lane a page: is any of its keys needed, and where does it lie
                 int y = -1;
                 if (lane < per_tile) {
-                    const long key = k0 + ((long)lane << c.page_shift);
-                    // the page's keys that are needed are its first ones (sinks, up to see_hi) or its last ones (window)
-                    if (key <= see_hi && (needed(key) || needed(min(key + page - 1, see_hi)))) {
+                    const int key = k0 + (lane << c.page_shift);
+                    // the page's keys that are needed are its first ones (sinks, up to the end) or its last ones (window)
+                    if (key < seen_any.end && (seen_any(key) || seen_any(min(key + page, seen_any.end) - 1))) {
                         const long r = cache_row(c, b, hk, key);
                         if (r >= 0)
                             y = (int)r;
@@ -442,7 +444,7 @@ __global__ void __launch_bounds__(Plan<E4M3, NT>::kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int key = 32 * i + lane;
-                    valid[i] = __ballot_sync(0xffffffffu, needed(k0 + key) && (pages >> (key >> c.page_shift) & 1));
+                    valid[i] = __ballot_sync(0xffffffffu, seen_any(k0 + key) && (pages >> (key >> c.page_shift) & 1));
                     all &= valid[i];
                 }
                 if (j >= STAGES && !(ok = wait_warp(&s.empty[stage], (j / STAGES - 1) & 1))) break;
@@ -485,9 +487,9 @@ __global__ void __launch_bounds__(Plan<E4M3, NT>::kThreads, 1)
                 int* rows_at = s.at[j & 1];
                 uint32_t there = 0;
                 if (i0 < kKeys) {
-                    const long key = (long)tiles[first + j] * kKeys + i0;
+                    const int key = tiles[first + j] * kKeys + i0;
                     long at = -1;
-                    if (needed(key)) {
+                    if (seen_any(key)) {
                         at = cache_row(c, b, hk, key);
                         if (at < 0) atomicOr(c.status, kStatusMissingPage);
                     }

@@ -4,30 +4,34 @@
 
 namespace titans {
 
-// The keys that the row at position p sees: j < sink_end, or begin <= j <= p.
+// Positions that the page table has room for, below 2^31.
+__device__ __forceinline__ int capacity(const CacheArgs& c) { return c.max_pages << c.page_shift; }
+
+// The keys that the row at position p sees, as far as the table has room for them: j < sink_end, or begin <= j < end.
 struct Seen {
-    long begin, sink_end;
+    int begin, end, sink_end;
+    __device__ bool operator()(int key) const { return key < end && (key >= begin || key < sink_end); }
 };
 __device__ __forceinline__ Seen seen_by(const AttendArgs& a, long p) {
-    const long begin = a.window ? max(0L, p - a.window + 1) : 0L;
-    return {begin, min((long)a.sinks, begin)};
+    const long cap = capacity(a.c), begin = a.window ? max(0L, p - a.window + 1) : 0L;
+    return {(int)min(begin, cap), (int)max(0L, min(p + 1, cap)), (int)min((long)min(a.sinks, capacity(a.c)), begin)};
+}
+// The keys that some row at positions p0..p1 sees: the widest of all bounds.
+__device__ __forceinline__ Seen seen_by_any(const AttendArgs& a, long p0, long p1) {
+    const Seen lo = seen_by(a, max(p0, 0L)), hi = seen_by(a, p1);
+    return {lo.begin, hi.end, hi.sink_end};
 }
 
-// The tiles of KEYS keys that rows at positions p0..p1 see: 0..head-1 and tail..end-1.
+// The tiles of KEYS keys that those keys lie in: 0..head-1 and from tail on, `count` together.
 struct Tiles {
     int head, tail, count;
     __device__ int operator[](int i) const { return i < head ? i : tail + i - head; }
 };
 template <int KEYS>
-__device__ __forceinline__ Tiles tiles_of(const AttendArgs& a, long p0, long p1) {
-    Tiles t{0, 0, 0};
-    if (p1 < 0) return t;
-    const long end = p1 / KEYS + 1;
-    t.tail = (int)(seen_by(a, max(p0, 0L)).begin / KEYS);
-    // the last row has the widest view of the sinks: those before its own window
-    t.head = (int)min((long)t.tail, (seen_by(a, p1).sink_end + KEYS - 1) / KEYS);
-    t.count = t.head + (int)end - t.tail;
-    return t;
+__device__ __forceinline__ Tiles tiles_of(const Seen& s) {
+    const int end = (s.end + KEYS - 1) / KEYS, tail = min(s.begin / KEYS, end);
+    const int head = min(tail, (min(s.sink_end, s.end) + KEYS - 1) / KEYS);
+    return {head, tail, head + end - tail};
 }
 
 // N consecutive values of a row of the pool.
@@ -35,12 +39,17 @@ template <int N, bool E4M3>
 __device__ __forceinline__ void load_row(const void* pool, const float* scales, long row, int col, int D, float (&x)[N]) {
     if constexpr (E4M3) {
         const float s = scales[row];
-        const uint16_t* p = reinterpret_cast<const uint16_t*>(static_cast<const uint8_t*>(pool) + row * D + col);
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) {
-            const float2 f = e4m3x2_to_float2(p[i]);
-            x[2 * i] = f.x * s;
-            x[2 * i + 1] = f.y * s;
+        const uint8_t* p = static_cast<const uint8_t*>(pool) + row * D + col;
+        uint32_t u;  // two or four of them
+        if constexpr (N == 4)
+            u = *reinterpret_cast<const uint32_t*>(p);
+        else
+            u = *reinterpret_cast<const uint16_t*>(p);
+        const float2 f = e4m3_to_float2<false>(u);
+        x[0] = f.x * s, x[1] = f.y * s;
+        if constexpr (N == 4) {
+            const float2 g = e4m3_to_float2<true>(u);
+            x[2] = g.x * s, x[3] = g.y * s;
         }
     } else {
         const __nv_bfloat162* p =
@@ -70,9 +79,9 @@ __device__ __noinline__ void attend_row(const AttendArgs& a, int b, int hk, cons
     }
     m = -INFINITY, l = 0.f;
     for (int i = first; i < last; ++i) {
-        const long j0 = (long)tiles[i] * KEYS;
-        for (long j = j0; j < j0 + KEYS && j <= p; ++j) {
-            if (j >= s.sink_end && j < s.begin) continue;
+        const int j0 = tiles[i] * KEYS;
+        for (int j = j0; j < min(j0 + KEYS, s.end); ++j) {
+            if (!s(j)) continue;
             const long at = cache_row(c, b, hk, j);
             if (at < 0) continue;
             float x[N], z = 0.f;

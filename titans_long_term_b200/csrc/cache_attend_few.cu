@@ -23,6 +23,7 @@
 // fp16 as 2^(z + log2 s - M), s the scale of the key's values and M the running maximum of z + log2 s, so that the largest
 // contribution is near 1 whatever the scales are; their sum takes them back by 1 / s, in fp32.
 #include <algorithm>
+#include <type_traits>
 
 #include "cache_attend.cuh"
 #include "ptx.cuh"
@@ -54,22 +55,14 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Two e4m3 values as fp16, exactly.
-__device__ __forceinline__ uint32_t half_of(uint32_t e4m3x2) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((uint16_t)e4m3x2, __NV_E4M3);
-    return h.x | (uint32_t)h.y << 16;
-}
-
-template <bool E4M3>
 constexpr int kBlock = 16;  // keys of a block
 
-// Blocks of keys of sequence b that its rows see.
-template <int KEYS>
-__device__ __forceinline__ Tiles blocks_of(const AttendArgs& a, int b) {
-    const int G = a.c.H / a.c.Hkv, n = min((int)a.c.T * G, cache_count(a.c, b) * G);
-    if (n <= 0) return Tiles{0, 0, 0};
+// The keys of sequence b that some of its rows see.
+__device__ __forceinline__ Seen keys_of(const AttendArgs& a, int b) {
+    const int n = cache_count(a.c, b);
+    if (n == 0) return Seen{0, 0, 0};
     const long start = a.c.starts[b];
-    return tiles_of<KEYS>(a, start, start + (n - 1) / G);
+    return seen_by_any(a, start, start + n - 1);
 }
 // The CTA of n whose share of `total` holds block x.
 __device__ __forceinline__ int owner(long x, long n, long total) { return (int)(((x + 1) * n - 1) / total); }
@@ -84,8 +77,8 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 // NQ: tiles of eight rows.
 template <int D, bool E4M3, int NQ>
 struct Few {
-    static constexpr int kKeys = kBlock<E4M3>, kSub = kKeys / 16;  // keys of a block, in sixteens
-    static constexpr int kWarps = NQ == 2 ? 8 : E4M3 ? 16 : 12;
+    static constexpr int kKeys = kBlock, kSub = kKeys / 16;  // keys of a block, in sixteens
+    static constexpr int kWarps = NQ == 2 ? 8 : 12;
     static constexpr int kRows = 8 * NQ;
     static constexpr int kBytes = kWarps * kRows * (D * (int)sizeof(float) + (int)sizeof(float2));
     static constexpr int kKP = D * (E4M3 ? 1 : 2) / 64;  // 16-byte pieces of a key row for each of four lanes
@@ -106,8 +99,8 @@ __device__ __forceinline__ void attend_head(const AttendArgs& a, int b, int hk, 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, q4 = lane & 3;
     const int G = c.H / c.Hkv, rows = (int)c.T * G, seen_rows = min(rows, cache_count(c, b) * G);
     const long start = c.starts[b];
-    const long see_hi = start + (seen_rows - 1) / G;  // keys that some row sees: see_lo..see_hi, and below sink_hi
-    const long see_lo = seen_by(a, start).begin, sink_hi = seen_by(a, see_hi).sink_end;
+    const Seen any = keys_of(a, b), every = seen_by(a, start);  // what some row sees; with `whole` below, what every row sees
+    const int every_begin = seen_by(a, start + (seen_rows - 1) / G).begin;
 
     // Q's rows 8 n + r as B fragments
     uint32_t q[NQ][KP * KW / 2][2];
@@ -157,87 +150,104 @@ __device__ __forceinline__ void attend_head(const AttendArgs& a, int b, int hk, 
             m[n][h] = -INFINITY;
         }
 
-    // The page of 16 keys from key0 on: -2 where no row sees any of them, -1 where the table has none. Only the load, so
-    // that nothing waits for it until row_of.
-    auto page_of = [&](long key0) -> int {
-        if (key0 > see_hi || (key0 + 15 < see_lo && key0 >= sink_hi)) return -2;
-        const long index = key0 >> c.page_shift;
-        return index < c.max_pages ? max(c.table[(long)b * c.max_pages + index], -1) : -1;
+    // The page of 16 keys from key0 on; -2 where no row sees any of them. Only the load, so that nothing waits for it
+    // until row_of.
+    const int* table = c.table + (long)b * c.max_pages;
+    auto page_of = [&](int key0) -> int {
+        if (key0 >= any.end || (key0 + 15 < any.begin && key0 >= any.sink_end)) return -2;
+        return max(table[key0 >> c.page_shift], -1);
     };
     // Row of the pool where they begin, or -1.
-    auto row_of = [&](int page, long key0) -> long {
+    auto row_of = [&](int page, int key0) -> int {
         if ((unsigned)page >= (unsigned)c.num_pages) {
             if (page != -2 && lane == 0) atomicOr(c.status, kStatusMissingPage);
             return -1;
         }
-        return (((long)page * c.Hkv + hk) << c.page_shift) + (key0 & ((1 << c.page_shift) - 1));
+        return ((page * c.Hkv + hk) << c.page_shift) + (key0 & ((1 << c.page_shift) - 1));  // rows are fewer than 2^31
     };
     uint4 kb[SUB][2][KP];
     uint4 vb[SUB][4][VG];
     float ks[SUB][2], vs[SUB][2];  // e4m3: scales of the keys r and r + 8
-    auto load_k = [&](const long (&at)[SUB]) {
-#pragma unroll
-        for (int s = 0; s < SUB; ++s)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint4* src = static_cast<const uint4*>(c.pk) + (at[s] + r + 8 * h) * (4 * KP) + q4;
-#pragma unroll
-                for (int i = 0; i < KP; ++i) kb[s][h][i] = at[s] >= 0 ? src[4 * i] : make_uint4(0, 0, 0, 0);
-                if constexpr (E4M3) ks[s][h] = at[s] >= 0 ? c.k_scale[at[s] + r + 8 * h] : 0.f;
-            }
-    };
-    // Values that no row sees are zeros: their weights are 0, and 0 times an infinity or NaN would not be.
-    auto load_v = [&](const long (&at)[SUB], long key0) {
-        const bool all = key0 + KEYS - 1 <= see_hi && (key0 >= see_lo || key0 + KEYS <= sink_hi);
+    auto load_k = [&](const int(&at)[SUB]) {
 #pragma unroll
         for (int s = 0; s < SUB; ++s) {
+            if (at[s] < 0) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int k = 2 * q4 + (e & 1) + (e >> 1) * 8;
-                bool there = at[s] >= 0;
-                if (!all) {
-                    const long key = key0 + 16 * s + k;
-                    there = there && key <= see_hi && (key >= see_lo || key < sink_hi);
+                for (int h = 0; h < 2; ++h) {
+                    ks[s][h] = 0.f;
+#pragma unroll
+                    for (int i = 0; i < KP; ++i) kb[s][h][i] = make_uint4(0, 0, 0, 0);
                 }
-                const char* src = static_cast<const char*>(c.pv) + (at[s] + k) * (D * (E4M3 ? 1 : 2)) + r * VB;
+                continue;
+            }
+            const uint4* src = static_cast<const uint4*>(c.pk) + (long)(at[s] + r) * (4 * KP) + q4;
 #pragma unroll
-                for (int g = 0; g < VG; ++g) {
-                    vb[s][e][g] = make_uint4(0, 0, 0, 0);
-                    if (there) {
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < KP; ++i) kb[s][h][i] = src[32 * KP * h + 4 * i];
+            if constexpr (E4M3) ks[s][0] = c.k_scale[at[s] + r], ks[s][1] = c.k_scale[at[s] + r + 8];
+        }
+    };
+    // Values that no row sees are zeros: their weights are 0, and 0 times an infinity or NaN would not be.
+    auto load_v = [&](const int(&at)[SUB], int key0) {
+#pragma unroll
+        for (int s = 0; s < SUB; ++s, key0 += 16) {
+            auto load = [&](auto all) {
+                const char* src = static_cast<const char*>(c.pv) + (long)(at[s] + 2 * q4) * (D * (E4M3 ? 1 : 2)) + r * VB;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int k = (e & 1) + (e >> 1) * 8;
+                    const bool there = all.value || any(key0 + 2 * q4 + k);
+#pragma unroll
+                    for (int g = 0; g < VG; ++g) {
+                        const char* p = src + k * (D * (E4M3 ? 1 : 2)) + g * 8 * VB;
+                        uint4& v = vb[s][e][g];
+                        if constexpr (!all.value) v = make_uint4(0, 0, 0, 0);
                         if constexpr (VB == 16) {
-                            vb[s][e][g] = *reinterpret_cast<const uint4*>(src + g * 8 * VB);
+                            if (there) v = *reinterpret_cast<const uint4*>(p);
                         } else {
-                            const uint2 u = *reinterpret_cast<const uint2*>(src + g * 8 * VB);
-                            vb[s][e][g].x = u.x, vb[s][e][g].y = u.y;
+                            uint2 u = make_uint2(0, 0);
+                            if (there) u = *reinterpret_cast<const uint2*>(p);
+                            v.x = u.x, v.y = u.y;
                         }
                     }
                 }
-            }
-            if constexpr (E4M3)
+            };
+            if (at[s] < 0) {
+                vs[s][0] = vs[s][1] = 0.f;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) vs[s][h] = at[s] >= 0 ? c.v_scale[at[s] + r + 8 * h] : 0.f;
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int g = 0; g < VG; ++g) vb[s][e][g] = make_uint4(0, 0, 0, 0);
+                continue;
+            }
+            if (key0 + 16 <= any.end && (key0 >= any.begin || key0 + 16 <= any.sink_end))
+                load(std::true_type{});
+            else
+                load(std::false_type{});
+            if constexpr (E4M3) vs[s][0] = c.v_scale[at[s] + r], vs[s][1] = c.v_scale[at[s] + r + 8];
         }
     };
 
     float o[VG][VE / 2][NQ][4] = {};
-    long at[SUB], at_next[SUB];
+    int at[SUB], at_next[SUB];
     int page[SUB];  // of the block after the next one
     auto pages_of = [&](int i) {
 #pragma unroll
-        for (int s = 0; s < SUB; ++s) page[s] = i < last ? page_of((long)tiles[i] * KEYS + 16 * s) : -2;
+        for (int s = 0; s < SUB; ++s) page[s] = i < last ? page_of(tiles[i] * KEYS + 16 * s) : -2;
     };
-    auto rows_of = [&](int i, long(&x)[SUB]) {
+    auto rows_of = [&](int i, int(&x)[SUB]) {
 #pragma unroll
-        for (int s = 0; s < SUB; ++s) x[s] = row_of(page[s], (long)tiles[i] * KEYS + 16 * s);
+        for (int s = 0; s < SUB; ++s) x[s] = row_of(page[s], tiles[i] * KEYS + 16 * s);
     };
     int i = first + warp;
     pages_of(i);
     rows_of(i, at);
     pages_of(i + W);
     load_k(at);
-    load_v(at, (long)tiles[i] * KEYS);
+    load_v(at, tiles[i] * KEYS);
     for (; i < last; i += W) {
-        const long key0 = (long)tiles[i] * KEYS;
+        const int key0 = tiles[i] * KEYS;
         rows_of(i + W, at_next);
         pages_of(i + 2 * W);
         float sc[SUB][NQ][4] = {};
@@ -251,7 +261,8 @@ __device__ __forceinline__ void attend_head(const AttendArgs& a, int b, int hk, 
                 for (int t = 0; t < KW / 2; ++t) {
                     uint32_t f[4];
                     if constexpr (E4M3) {
-                        f[0] = half_of(x[t]), f[1] = half_of(y[t]), f[2] = half_of(x[t] >> 16), f[3] = half_of(y[t] >> 16);
+                        f[0] = e4m3_to_half2<false>(x[t]), f[1] = e4m3_to_half2<false>(y[t]);
+                        f[2] = e4m3_to_half2<true>(x[t]), f[3] = e4m3_to_half2<true>(y[t]);
                     } else {
                         f[0] = x[2 * t], f[1] = y[2 * t], f[2] = x[2 * t + 1], f[3] = y[2 * t + 1];
                     }
@@ -266,7 +277,7 @@ __device__ __forceinline__ void attend_head(const AttendArgs& a, int b, int hk, 
                 }
             }
         // Scores in log2 units (e4m3: plus that of the value's scale); -infinity where the row does not see the key
-        bool whole = key0 >= seen_by(a, see_hi).begin && key0 + KEYS - 1 <= start;
+        bool whole = key0 >= every_begin && key0 + KEYS <= every.end;
 #pragma unroll
         for (int s = 0; s < SUB; ++s) whole = whole && at[s] >= 0;
         float inv[SUB][2], top[NQ][2];
@@ -288,9 +299,8 @@ __device__ __forceinline__ void attend_head(const AttendArgs& a, int b, int hk, 
                         float& x = sc[s][n][2 * e + h];
                         x = fmaf(x, k_scale * scale[n][h], v_log);
                         if (!whole) {
-                            const long key = key0 + 16 * s + 8 * e + r, p = start + (8 * n + 2 * q4 + h) / G;
-                            const Seen v = seen_by(a, p);
-                            if (at[s] < 0 || key > p || (key < v.begin && key >= v.sink_end)) x = -INFINITY;
+                            const Seen v = seen_by(a, start + (8 * n + 2 * q4 + h) / G);
+                            if (at[s] < 0 || !v(key0 + 16 * s + 8 * e + r)) x = -INFINITY;
                         }
                         top[n][h] = fmaxf(top[n][h], x);
                     }
@@ -349,7 +359,12 @@ __device__ __forceinline__ void attend_head(const AttendArgs& a, int b, int hk, 
                 for (int e = 0; e < VE / 2; ++e) {
                     uint32_t x[4], f[4];  // values 2 e, 2 e + 1 of the four keys
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) x[k] = E4M3 ? half_of(v[k][e >> 1] >> (e & 1) * 16) : v[k][e];
+                    for (int k = 0; k < 4; ++k) {
+                        if constexpr (!E4M3)
+                            x[k] = v[k][e];
+                        else
+                            x[k] = e & 1 ? e4m3_to_half2<true>(v[k][e >> 1]) : e4m3_to_half2<false>(v[k][e >> 1]);
+                    }
                     f[0] = __byte_perm(x[0], x[1], 0x5410), f[1] = __byte_perm(x[0], x[1], 0x7632);
                     f[2] = __byte_perm(x[2], x[3], 0x5410), f[3] = __byte_perm(x[2], x[3], 0x7632);
 #pragma unroll
@@ -362,7 +377,7 @@ __device__ __forceinline__ void attend_head(const AttendArgs& a, int b, int hk, 
                 }
             }
         }
-        load_v(at_next, (long)tiles[i + W] * KEYS);
+        load_v(at_next, tiles[i + W] * KEYS);
 #pragma unroll
         for (int s = 0; s < SUB; ++s) at[s] = at_next[s];
     }
@@ -424,7 +439,7 @@ __device__ __forceinline__ void attend_head(const AttendArgs& a, int b, int hk, 
 
 template <int D, bool E4M3, int NQ>
 __global__ void __launch_bounds__(Few<D, E4M3, NQ>::kWarps * 32, 1) attend_few_kernel(AttendArgs a) {
-    constexpr int W = Few<D, E4M3, NQ>::kWarps, KEYS = kBlock<E4M3>;
+    constexpr int W = Few<D, E4M3, NQ>::kWarps, KEYS = kBlock;
     extern __shared__ __align__(16) float smem[];  // outputs [warps][rows][D], then maxima and sums [warps][rows]
     __shared__ long warp_sums[W];
     __shared__ long found[2];  // sequence where the share's first block lies, and where its blocks begin
@@ -437,7 +452,7 @@ __global__ void __launch_bounds__(Few<D, E4M3, NQ>::kWarps * 32, 1) attend_few_k
         const long x0 = total * blockIdx.x / gridDim.x;
         for (int b0 = 0; b0 < c.B; b0 += W * 32) {
             const int b = b0 + threadIdx.x;
-            const long n = b < c.B ? (long)blocks_of<KEYS>(a, b).count * c.Hkv : 0;
+            const long n = b < c.B ? (long)tiles_of<KEYS>(keys_of(a, b)).count * c.Hkv : 0;
             long sum = n;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -452,6 +467,10 @@ __global__ void __launch_bounds__(Few<D, E4M3, NQ>::kWarps * 32, 1) attend_few_k
                 if (w < warp) begin += warp_sums[w];
                 base += warp_sums[w];
             }
+            if (blockIdx.x == 0 && b < c.B) {
+                const int tokens = cache_count(c, b);
+                if (tokens > 0 && (long)c.starts[b] + tokens > capacity(c)) atomicOr(c.status, kStatusMissingPage);
+            }
             if (pass && x0 >= begin && x0 < begin + n) found[0] = b, found[1] = begin;
             if (pass && blockIdx.x == 0 && b < c.B) a.begins[b] = begin;
         }
@@ -463,10 +482,10 @@ __global__ void __launch_bounds__(Few<D, E4M3, NQ>::kWarps * 32, 1) attend_few_k
     const long x_begin = total * blockIdx.x / gridDim.x, x_end = total * (blockIdx.x + 1) / gridDim.x;
     if (x_begin == x_end) return;
     int b = (int)found[0];
-    Tiles tiles = blocks_of<KEYS>(a, b);
+    Tiles tiles = tiles_of<KEYS>(keys_of(a, b));
     int hk = (int)((x_begin - found[1]) / tiles.count), first = (int)((x_begin - found[1]) % tiles.count);
     for (long x = x_begin; x < x_end;) {
-        while (tiles.count == 0 || hk == c.Hkv) hk = 0, tiles = blocks_of<KEYS>(a, ++b);
+        while (tiles.count == 0 || hk == c.Hkv) hk = 0, tiles = tiles_of<KEYS>(keys_of(a, ++b));
         const int last = (int)min((long)tiles.count, first + x_end - x);
         attend_head<D, E4M3, NQ>(a, b, hk, tiles, first, last, (long)blockIdx.x * 2 + (x > x_begin), smem);
         x += last - first;
@@ -483,7 +502,7 @@ __global__ void __launch_bounds__(128) join_kernel(AttendArgs a, int ctas) {
     const long at = (long)blockIdx.x * 4 + (threadIdx.x >> 5), unit = at / rows;
     if (unit >= (long)c.B * c.Hkv) return;
     const int row = (int)(at % rows), b = (int)(unit / c.Hkv), hk = (int)(unit % c.Hkv);
-    const int n = blocks_of<KEYS>(a, b).count;
+    const int n = tiles_of<KEYS>(keys_of(a, b)).count;
     float top = -INFINITY, sum = 0.f, acc[N] = {};
     if (n > 0) {
         const long total = a.begins[c.B], x0 = a.begins[b] + (long)hk * n;
