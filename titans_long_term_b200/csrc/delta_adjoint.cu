@@ -32,11 +32,14 @@ __global__ void __launch_bounds__(RW * 2 + kProducers, 1)
         const Tok* k = static_cast<const Tok*>(a.k) + delta_key_head(a, unit) * a.T * D;
         const Tok* q = static_cast<const Tok*>(a.q) + delta_key_head(a, unit) * a.T * D;
         const Tok* dy = static_cast<const Tok*>(g.dy) + unit * a.T * D + row_base;
+        Producer<D, RW, Tok, 2, true> next;
+        auto fetch = [&](int c) { next.fetch(k, q, dy, (long)c * kC, (int)min((long)kC, len - (long)c * kC), p); };
+        if (used > 0) fetch(used - 1);
         for (int c = used - 1, i = 0; c >= 0; --c, ++i) {
-            const long t0 = (long)c * kC;
             if (i >= 2) bar_sync(3 + (i & 1), kThreads);
-            fill_stage<D, RW, Tok, 2, true>(stages[i & 1], rec[c], k, q, dy, t0, (int)min((long)kC, len - t0), p);
+            next.store(stages[i & 1], rec[c], p);
             bar_arrive(1 + (i & 1), kThreads);
+            if (c > 0) fetch(c - 1);
         }
         return;
     }
@@ -77,13 +80,9 @@ __global__ void __launch_bounds__(RW * 2 + kProducers, 1)
             for (int kt = 0; kt < D / 16; ++kt) {
                 uint32_t hi[4], lo[4];
                 split_a<D / 8>(w, kt, s0, s1, hi, lo);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t f[NP][4];
-#pragma unroll
-                    for (int e = 0; e < NP; ++e) frag_b<D>(f[e], ks + e * kC * D * 2, j * 16, kt * 16, lane);
-                    mma_pieces<NP>(x[2 * j], x[2 * j + 1], hi, lo, f);
-                }
+                mma_row<2, NP, 0, 4>(x, hi, lo, [&](uint32_t(&f)[4], int j, int e) {
+                    frag_b<D>(f, ks + e * kC * D * 2, j * 16, kt * 16, lane);
+                });
             }
         }
         {  // dE^T = l (A K^T) + dY^T P
@@ -100,25 +99,19 @@ __global__ void __launch_bounds__(RW * 2 + kProducers, 1)
             float top0, top1;
             row_tops<8>(v, top0, top1);
             const float s0 = pow2_scale(top0, i0), s1 = pow2_scale(top1, i1);
-#pragma unroll
-            for (int kt = 0; kt < 4; ++kt) {
+            unrolled<4>([&](auto kt) {  // P_ij, i >= j
                 uint32_t hi[4], lo[4];
                 split_a<8>(v, kt, s0, s1, hi, lo);
-#pragma unroll
-                for (int j = 0; j <= kt; ++j) {  // P_ij, i >= j
-                    uint32_t f[2][4];
-                    frag_bt<kC>(f[0], ps, j * 16, kt * 16, lane);
-                    frag_bt<kC>(f[1], ps + kC * kC * 2, j * 16, kt * 16, lane);
-                    mma_pieces<2>(acc[2 * j], acc[2 * j + 1], hi, lo, f);
-                }
-            }
+                mma_triangle<kt, false, 2, 2>(acc, hi, lo, [&](uint32_t(&f)[4], int j, int e) {
+                    frag_bt<kC>(f, ps + e * kC * kC * 2, j * 16, kt * 16, lane);
+                });
+            });
 #pragma unroll
             for (int t = 0; t < 8; ++t) {
                 x[t][0] += acc[t][0] * i0 * p_inv, x[t][1] += acc[t][1] * i0 * p_inv;
                 x[t][2] += acc[t][2] * i1 * p_inv, x[t][3] += acc[t][3] * i1 * p_inv;
             }
             // A <- gamma_C A + (gamma dY)^T Q
-            const float decay = s.gamma[kC - 1];
 #pragma unroll
             for (int t = 0; t < 8; ++t) {
                 const float2 gm = *reinterpret_cast<const float2*>(s.gamma + 8 * t + col2);
@@ -126,27 +119,7 @@ __global__ void __launch_bounds__(RW * 2 + kProducers, 1)
             }
             row_tops<8>(v, top0, top1);
             const float r0 = pow2_scale(top0, i0), r1 = pow2_scale(top1, i1);
-            i0 *= q_inv, i1 *= q_inv;
-            uint32_t hi[4][4], lo[4][4];
-#pragma unroll
-            for (int kt = 0; kt < 4; ++kt) split_a<8>(v, kt, r0, r1, hi[kt], lo[kt]);
-#pragma unroll
-            for (int j = 0; j < D / 16; ++j) {
-                float acc[2][4] = {};
-#pragma unroll
-                for (int kt = 0; kt < 4; ++kt) {
-                    uint32_t f[NP][4];
-#pragma unroll
-                    for (int e = 0; e < NP; ++e) frag_bt<D>(f[e], qs + e * kC * D * 2, j * 16, kt * 16, lane);
-                    mma_pieces<NP>(acc[0], acc[1], hi[kt], lo[kt], f);
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float(&u)[4] = w[2 * j + h];
-                    u[0] = fmaf(u[0], decay, acc[h][0] * i0), u[1] = fmaf(u[1], decay, acc[h][1] * i0);
-                    u[2] = fmaf(u[2], decay, acc[h][2] * i1), u[3] = fmaf(u[3], decay, acc[h][3] * i1);
-                }
-            }
+            add_outer<D, NP>(w, s.gamma[kC - 1], v, r0, r1, i0 * q_inv, i1 * q_inv, qs, lane);
         }
         {  // dR^T = dE^T - (beta dE)^T N
             float r[8][4], acc[8][4] = {};
@@ -158,18 +131,13 @@ __global__ void __launch_bounds__(RW * 2 + kProducers, 1)
             float top0, top1;
             row_tops<8>(r, top0, top1);
             const float s0 = pow2_scale(top0, i0), s1 = pow2_scale(top1, i1);
-#pragma unroll
-            for (int kt = 0; kt < 4; ++kt) {
+            unrolled<4>([&](auto kt) {  // N_ij, i > j
                 uint32_t hi[4], lo[4];
                 split_a<8>(r, kt, s0, s1, hi, lo);
-#pragma unroll
-                for (int j = 0; j <= kt; ++j) {  // N_ij, i > j
-                    uint32_t f[2][4];
-                    frag_bt<kC>(f[0], ns, j * 16, kt * 16, lane);
-                    frag_bt<kC>(f[1], ns + kC * kC * 2, j * 16, kt * 16, lane);
-                    mma_pieces<2>(acc[2 * j], acc[2 * j + 1], hi, lo, f);
-                }
-            }
+                mma_triangle<kt, false, 2, 2>(acc, hi, lo, [&](uint32_t(&f)[4], int j, int e) {
+                    frag_bt<kC>(f, ns + e * kC * kC * 2, j * 16, kt * 16, lane);
+                });
+            });
             float* o = g.dr + (unit * chunks + c) * kC * D + row;
 #pragma unroll
             for (int t = 0; t < 8; ++t) {
@@ -187,27 +155,7 @@ __global__ void __launch_bounds__(RW * 2 + kProducers, 1)
             float top0, top1;
             row_tops<8>(x, top0, top1);
             const float s0 = pow2_scale(top0, i0), s1 = pow2_scale(top1, i1);
-            i0 *= -k_inv, i1 *= -k_inv;
-            uint32_t hi[4][4], lo[4][4];
-#pragma unroll
-            for (int kt = 0; kt < 4; ++kt) split_a<8>(x, kt, s0, s1, hi[kt], lo[kt]);
-#pragma unroll
-            for (int j = 0; j < D / 16; ++j) {
-                float acc[2][4] = {};
-#pragma unroll
-                for (int kt = 0; kt < 4; ++kt) {
-                    uint32_t f[NP][4];
-#pragma unroll
-                    for (int e = 0; e < NP; ++e) frag_bt<D>(f[e], ks + e * kC * D * 2, j * 16, kt * 16, lane);
-                    mma_pieces<NP>(acc[0], acc[1], hi[kt], lo[kt], f);
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float(&u)[4] = w[2 * j + h];
-                    u[0] = fmaf(acc[h][0], i0, u[0]), u[1] = fmaf(acc[h][1], i0, u[1]);
-                    u[2] = fmaf(acc[h][2], i1, u[2]), u[3] = fmaf(acc[h][3], i1, u[3]);
-                }
-            }
+            add_outer<D, NP>(w, 1.f, x, s0, s1, -k_inv * i0, -k_inv * i1, ks, lane);
         }
         if (c >= 2) bar_arrive(3 + (i & 1), kThreads);
     }

@@ -35,11 +35,14 @@ __global__ void __launch_bounds__(RW * 2 + kProducers, 1)
         const Tok* k = static_cast<const Tok*>(a.k) + delta_key_head(a, unit) * a.T * D;
         const Tok* q = static_cast<const Tok*>(a.q) + delta_key_head(a, unit) * a.T * D;
         const Tok* v = static_cast<const Tok*>(a.v) + unit * a.T * D + row_base;
+        Producer<D, RW, Tok, NP, !STATES> next;
+        auto fetch = [&](int c) { next.fetch(k, q, v, (long)c * kC, (int)min((long)kC, len - (long)c * kC), p); };
+        if (used > 0) fetch(0);
         for (int c = 0; c < used; ++c) {
-            const long t0 = (long)c * kC;
             if (c >= 2) bar_sync(3 + (c & 1), kThreads);
-            fill_stage<D, RW, Tok, NP, !STATES>(stages[c & 1], rec[c], k, q, v, t0, (int)min((long)kC, len - t0), p);
+            next.store(stages[c & 1], rec[c], p);
             bar_arrive(1 + (c & 1), kThreads);
+            if (c + 1 < used) fetch(c + 1);
         }
     } else {  // --------------------------------------------------------- sixteen rows of the state a warp
         const int row = row_base + warp * 16 + (lane >> 2), col2 = 2 * (lane & 3);
@@ -76,23 +79,12 @@ __global__ void __launch_bounds__(RW * 2 + kProducers, 1)
                 for (int kt = 0; kt < D / 16; ++kt) {
                     uint32_t hi[4], lo[4];
                     split_a<D / 8>(w, kt, s0, s1, hi, lo);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t f[NP][4];
-#pragma unroll
-                        for (int e = 0; e < NP; ++e) frag_b<D>(f[e], ks + e * kC * D * 2, j * 16, kt * 16, lane);
-                        mma_pieces<NP>(x[2 * j], x[2 * j + 1], hi, lo, f);
-                        if constexpr (!STATES) {
-#pragma unroll
-                            for (int e = 0; e < NP; ++e) frag_b<D>(f[e], qs + e * kC * D * 2, j * 16, kt * 16, lane);
-                            if constexpr (NP == 2) {
-                                mma_pieces<NP>(y[2 * j], y[2 * j + 1], hi, lo, f);
-                            } else {  // y is rounded to bf16: 11 bits of W are enough
-                                mma16816(y[2 * j], hi, f[0][0], f[0][1]);
-                                mma16816(y[2 * j + 1], hi, f[0][2], f[0][3]);
-                            }
-                        }
-                    }
+                    auto from = [&](uint32_t tile) {
+                        return [=](uint32_t(&f)[4], int j, int e) { frag_b<D>(f, tile + e * kC * D * 2, j * 16, kt * 16, lane); };
+                    };
+                    mma_row<2, NP, 0, 4>(x, hi, lo, from(ks));
+                    // y is rounded to the tokens' type: 11 bits of W are enough for bf16
+                    if constexpr (!STATES) mma_row<NP, NP, 0, 4>(y, hi, lo, from(qs));
                 }
             }
             // X^T = V^T - gamma W0 K^T (row: value, column: token), and Y's share of W0
@@ -120,18 +112,13 @@ __global__ void __launch_bounds__(RW * 2 + kProducers, 1)
                 row_tops<8>(r, top0, top1);
                 const float s0 = pow2_scale(top0, i0), s1 = pow2_scale(top1, i1);
                 float acc[8][4] = {};
-#pragma unroll
-                for (int kt = 0; kt < 4; ++kt) {
+                unrolled<4>([&](auto kt) {
                     uint32_t hi[4], lo[4];
                     split_a<8>(r, kt, s0, s1, hi, lo);
-#pragma unroll
-                    for (int j = kt; j < 4; ++j) {
-                        uint32_t f[2][4];
-                        frag_b<kC>(f[0], ns, j * 16, kt * 16, lane);
-                        frag_b<kC>(f[1], ns + kC * kC * 2, j * 16, kt * 16, lane);
-                        mma_pieces<2>(acc[2 * j], acc[2 * j + 1], hi, lo, f);
-                    }
-                }
+                    mma_triangle<kt, true, 2, 2>(acc, hi, lo, [&](uint32_t(&f)[4], int j, int e) {
+                        frag_b<kC>(f, ns + e * kC * kC * 2, j * 16, kt * 16, lane);
+                    });
+                });
 #pragma unroll
                 for (int t = 0; t < 8; ++t) {
                     x[t][0] -= acc[t][0] * i0 * n_inv, x[t][1] -= acc[t][1] * i0 * n_inv;
@@ -155,23 +142,13 @@ __global__ void __launch_bounds__(RW * 2 + kProducers, 1)
                 row_tops<8>(x, top0, top1);
                 const float s0 = pow2_scale(top0, i0), s1 = pow2_scale(top1, i1);
                 float acc[8][4] = {};
-#pragma unroll
-                for (int kt = 0; kt < 4; ++kt) {
+                unrolled<4>([&](auto kt) {
                     uint32_t hi[4], lo[4];
                     split_a<8>(x, kt, s0, s1, hi, lo);
-#pragma unroll
-                    for (int j = kt; j < 4; ++j) {
-                        uint32_t f[NP][4];
-#pragma unroll
-                        for (int e = 0; e < NP; ++e) frag_b<kC>(f[e], ps + e * kC * kC * 2, j * 16, kt * 16, lane);
-                        if constexpr (NP == 2) {
-                            mma_pieces<NP>(acc[2 * j], acc[2 * j + 1], hi, lo, f);
-                        } else {
-                            mma16816(acc[2 * j], hi, f[0][0], f[0][1]);
-                            mma16816(acc[2 * j + 1], hi, f[0][2], f[0][3]);
-                        }
-                    }
-                }
+                    mma_triangle<kt, true, NP, NP>(acc, hi, lo, [&](uint32_t(&f)[4], int j, int e) {
+                        frag_b<kC>(f, ps + e * kC * kC * 2, j * 16, kt * 16, lane);
+                    });
+                });
 #pragma unroll
                 for (int t = 0; t < 8; ++t) {  // into V's place, whose columns only this warp reads
                     float* v0 = vs + (8 * t + col2) * S::kVLd;
@@ -191,28 +168,7 @@ __global__ void __launch_bounds__(RW * 2 + kProducers, 1)
                 float top0, top1;
                 row_tops<8>(x, top0, top1);
                 const float s0 = pow2_scale(top0, i0), s1 = pow2_scale(top1, i1);
-                i0 *= k_inv, i1 *= k_inv;
-                const float decay = s.gamma[kC - 1];
-                uint32_t hi[4][4], lo[4][4];
-#pragma unroll
-                for (int kt = 0; kt < 4; ++kt) split_a<8>(x, kt, s0, s1, hi[kt], lo[kt]);
-#pragma unroll
-                for (int j = 0; j < D / 16; ++j) {
-                    float acc[2][4] = {};
-#pragma unroll
-                    for (int kt = 0; kt < 4; ++kt) {
-                        uint32_t f[NP][4];
-#pragma unroll
-                        for (int e = 0; e < NP; ++e) frag_bt<D>(f[e], ks + e * kC * D * 2, j * 16, kt * 16, lane);
-                        mma_pieces<NP>(acc[0], acc[1], hi[kt], lo[kt], f);
-                    }
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float(&u)[4] = w[2 * j + h];
-                        u[0] = fmaf(u[0], decay, acc[h][0] * i0), u[1] = fmaf(u[1], decay, acc[h][1] * i0);
-                        u[2] = fmaf(u[2], decay, acc[h][2] * i1), u[3] = fmaf(u[3], decay, acc[h][3] * i1);
-                    }
-                }
+                add_outer<D, NP>(w, s.gamma[kC - 1], x, s0, s1, i0 * k_inv, i1 * k_inv, ks, lane);
             }
             if constexpr (!STATES) {  // two lanes a token: 32 or 64 bytes of its row
                 __syncwarp();
