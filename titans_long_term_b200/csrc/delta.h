@@ -23,7 +23,7 @@ cudaError_t launch_delta_tokens(const DeltaArgs& a, cudaStream_t st);
 // The chunked path. Per (unit, chunk) record of delta_chunk_bytes(), written by the first kernel and read by the
 // others (delta_prepare.cu); units * ceil(T / 64) records.
 size_t delta_chunk_bytes();
-cudaError_t launch_delta_prepare(const DeltaArgs& a, void* chunks, cudaStream_t st);
+cudaError_t launch_delta_prepare(const DeltaArgs& a, void* chunks, bool backward, cudaStream_t st);
 // The state's way through the chunks, and y (delta_chunks.cu). With `states` it writes, in place of y and
 // the final state, every chunk's start state [units][chunks][d][d] and residuals eps [units][chunks][64][d], fp32.
 struct DeltaStates {

@@ -131,7 +131,7 @@ titans_status_t titans_delta_forward(const titans_delta_config* cfg, const void*
     const titans::DeltaArgs a = make_args(cfg, k, q, v, g, beta, lengths, T, W, attn, y);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (T <= kTokens) return launched(titans::launch_delta_tokens(a, st));
-    const cudaError_t e = titans::launch_delta_prepare(a, workspace, st);
+    const cudaError_t e = titans::launch_delta_prepare(a, workspace, false, st);
     return launched(e != cudaSuccess ? e : titans::launch_delta_chunks(a, workspace, nullptr, st));
 }
 
@@ -180,7 +180,7 @@ titans_status_t titans_delta_backward(const titans_delta_config* cfg, const void
     o.adj = reinterpret_cast<float*>(ws + at.adj);
     o.dr = reinterpret_cast<float*>(ws + at.dr);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = titans::launch_delta_prepare(a, ws, st);
+    cudaError_t e = titans::launch_delta_prepare(a, ws, true, st);
     if (e == cudaSuccess) e = titans::launch_delta_chunks(a, ws, &o.fwd, st);
     if (e == cudaSuccess) e = titans::launch_delta_adjoint(a, ws, o, st);
     if (e == cudaSuccess) e = titans::launch_delta_grads(a, ws, o, st);

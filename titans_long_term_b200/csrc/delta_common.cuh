@@ -18,6 +18,7 @@
 #include <cuda_fp16.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "delta.h"
 #include "ptx.cuh"
@@ -28,7 +29,7 @@ constexpr int kC = 64;  // tokens of a chunk
 
 // What the first kernel leaves of a chunk for the others, in the workspace.
 struct DeltaChunk {
-    __half N[2][kC * kC];  // pieces hi, lo; rows of 128 bytes, 16-byte blocks swizzled as sw64()
+    __half N[2][kC * kC];  // pieces hi, lo; rows of 128 bytes, swizzled as swz<64>(), only in_lower_blocks()
     __half P[2][kC * kC];
     float gamma[kC], rest[kC], beta[kC];  // exp(G_i), exp(G_C - G_i), beta_i
     float k_scale, q_scale;               // powers of two that the tiles of K and Q are multiplied by
@@ -38,6 +39,13 @@ struct DeltaChunk {
     float pad[122];
 };
 static_assert(sizeof(DeltaChunk) % 1024 == 0, "chunks stay 1 KiB aligned");
+
+// Whether 16-byte block i of the pieces of such a tile lies on or below the diagonal in blocks of 16 x 16. The others are neither
+// written nor read.
+__device__ __forceinline__ bool in_lower_blocks(int i) {
+    const int row = (i >> 3) & (kC - 1), block = (i & 7) ^ (row & 7);
+    return block >> 1 <= row >> 4;
+}
 
 // exp(G_i - G_j) for j <= i, 0 where a decay of 0 lies between.
 __device__ __forceinline__ float decay_between(const float* ghi, const float* glo, const int* zeros, int i, int j) {
@@ -193,6 +201,15 @@ __device__ __forceinline__ double warp_prefix(double x, int lane) {
         if (lane >= s) x += y;
     }
     return x;
+}
+
+// f(integral constant) for 0 .. N - 1.
+template <int N, typename F>
+__device__ __forceinline__ void unrolled(F f) {
+    if constexpr (N > 0) {
+        unrolled<N - 1>(f);
+        f(std::integral_constant<int, N - 1>{});
+    }
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {

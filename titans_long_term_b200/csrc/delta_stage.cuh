@@ -1,7 +1,5 @@
 // Stages of the two serial kernels of the chunked gated delta rule and the warps that fill them.
 #pragma once
-#include <type_traits>
-
 #include "delta_common.cuh"
 
 namespace titans {
@@ -53,15 +51,6 @@ __device__ __forceinline__ void mma_triangle(float (&acc)[8][4], const uint32_t 
                                              Fragment fragment) {
     mma_row<NA, NB, LOWER ? KT : 0, LOWER ? 4 : KT + 1>(acc, hi, lo, fragment);
 }
-// f(integral constant) for 0 .. N - 1.
-template <int N, typename F>
-__device__ __forceinline__ void unrolled(F f) {
-    if constexpr (N > 0) {
-        unrolled<N - 1>(f);
-        f(std::integral_constant<int, N - 1>{});
-    }
-}
-
 // w[row][.] = decay w[row][.] + sum over the 64 tokens of t[row][token] B[token][.]; t's two rows are scaled by s0, s1 on the way
 // and the products by i0, i1. B: NB pieces of a [64][D] tile at `tile`.
 template <int D, int NB>
@@ -143,10 +132,10 @@ struct Producer {
     // The fetched tokens and record r into stage s.
     __device__ __forceinline__ void store(Stage<D, RW, NP, PP>& s, const DeltaChunk& r, int p) {
         for (int i = p; i < (int)sizeof(r.N) / 16; i += kProducers)
-            cp_async16(smem_u32(s.n) + i * 16, reinterpret_cast<const uint4*>(r.N) + i);
+            if (in_lower_blocks(i)) cp_async16(smem_u32(s.n) + i * 16, reinterpret_cast<const uint4*>(r.N) + i);
         if constexpr (WITH_Q)
             for (int i = p; i < PP * kC * kC / 8; i += kProducers)
-                cp_async16(smem_u32(s.p) + i * 16, reinterpret_cast<const uint4*>(r.P) + i);
+                if (in_lower_blocks(i)) cp_async16(smem_u32(s.p) + i * 16, reinterpret_cast<const uint4*>(r.P) + i);
         for (int i = p; i < 3 * kC / 4; i += kProducers)
             cp_async16(smem_u32(s.gamma) + i * 16, reinterpret_cast<const uint4*>(r.gamma) + i);
         if (p < 6) s.scal[p] = (&r.k_scale)[p];
