@@ -1,37 +1,51 @@
 // Gated delta rule, second kernel of the chunked path: the state's way through the chunks, and y.
 //
-// What is serial is the state: each chunk's writes need it (X = V - gamma K W0^T). Rows of W are independent, so
-// a warp keeps sixteen of them in registers as the accumulator of its tensor-core products, which is also the layout
-// of their next A operand: per chunk it takes W0 K^T and W0 Q^T, E^T from N, P E, and adds (l E)^T K to W, without
-// exchanging anything with other warps and without W ever leaving registers. A CTA has 64 rows (32 in
-// fp32 mode at d = 128), four or two such warps, and four producer warps that bring the next chunk's K, Q, V, N
-// and P into a second stage of shared memory meanwhile, the tokens split into fp16 pieces on the way.
-//
-// The serial chain bounds it: with few units most SMs have one warp per tensor core, which runs
-// 448 (d = 64) or 816 (d = 128) m16n8k16 products per chunk one after another.
+// What is serial is the state: each chunk's writes need it (X = V - gamma K W0^T), and the next chunk needs them. Rows of
+// W are independent, so sixteen of them stay with one pair of warps from the first chunk to the last, in registers, as the
+// accumulators of tensor-core products, which is also the layout of their next A operand; nothing is exchanged with other
+// rows. The chain of a chunk bounds this kernel, with few units all the more (a warp on each tensor core, its
+// steps one after another), so it is kept short:
+//   - a pair halves it: each warp has half of W's columns, adds up W0 K^T over them and hands the other warp its
+//     tokens' part; then each has half of the tokens (the second half's eps need the first half's beta X), and gives the
+//     other the fragments of l E for its columns (Exchange in delta_stage.cuh);
+//   - a third warp of the same rows takes what the next chunk does not wait for: Y = gamma Q W0^T + P E, its gate and
+//     its stores, from the same fragments;
+//   - four producer warps bring the next chunk's K, Q, V, N and P into a second stage of shared memory meanwhile, the tokens
+//     split into fp16 pieces on the way.
 #include "delta_stage.cuh"
 
 namespace titans {
 namespace {
 
+// Named barriers; all threads take part in the stages', a group's two or three warps in its own.
+constexpr int kFull = 0, kFree = 2, kPair = 4, kOutFull = 8, kOutFree = 12;
+
+template <int D, int RW, bool STATES>
+struct Warps {
+    static constexpr int kGroups = RW / 16, kChain = 2 * kGroups, kOut = STATES ? 0 : kGroups;
+    static constexpr int kThreads = (kChain + kOut) * 32 + kProducers;
+    static_assert(kGroups <= 4, "sixteen barriers");
+};
+
 template <int D, int RW, typename Tok, bool STATES>
-__global__ void __launch_bounds__(RW * 2 + kProducers, 1)
+__global__ void __launch_bounds__(Warps<D, RW, STATES>::kThreads, 1)
     delta_chunks_kernel(DeltaArgs a, const DeltaChunk* recs, int chunks, DeltaStates st) {
-    constexpr int NP = sizeof(Tok) == 4 ? 2 : 1, NW = RW / 16, kThreads = NW * 32 + kProducers;
+    using T = Warps<D, RW, STATES>;
+    constexpr int NP = sizeof(Tok) == 4 ? 2 : 1, kThreads = T::kThreads;
     using S = Stage<D, RW, NP, NP>;
     extern __shared__ __align__(1024) unsigned char smem[];
     S* stages = reinterpret_cast<S*>(smem);
+    Exchange<D, NP>* exchanges = reinterpret_cast<Exchange<D, NP>*>(smem + 2 * sizeof(S));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int kSlices = D / RW;
     const long unit = blockIdx.x / kSlices;
     const int row_base = (int)(blockIdx.x % kSlices) * RW;
     const long b = unit / a.H, len = delta_length(a, b);
-    const int used = (int)((len + kC - 1) / kC);
+    const int used = (int)((len + kC - 1) / kC), col2 = 2 * (lane & 3);
     const DeltaChunk* rec = recs + unit * chunks;
-    // barriers 1, 2: stage filled; 3, 4: stage free
 
-    if (warp >= NW) {  // ------------------------------------------------ producers
-        const int p = tid - NW * 32;
+    if (warp >= T::kChain + T::kOut) {  // ------------------------------ producers
+        const int p = tid - (T::kChain + T::kOut) * 32;
         const Tok* k = static_cast<const Tok*>(a.k) + delta_key_head(a, unit) * a.T * D;
         const Tok* q = static_cast<const Tok*>(a.q) + delta_key_head(a, unit) * a.T * D;
         const Tok* v = static_cast<const Tok*>(a.v) + unit * a.T * D + row_base;
@@ -39,17 +53,20 @@ __global__ void __launch_bounds__(RW * 2 + kProducers, 1)
         auto fetch = [&](int c) { next.fetch(k, q, v, (long)c * kC, (int)min((long)kC, len - (long)c * kC), p); };
         if (used > 0) fetch(0);
         for (int c = 0; c < used; ++c) {
-            if (c >= 2) bar_sync(3 + (c & 1), kThreads);
+            if (c >= 2) bar_sync(kFree + (c & 1), kThreads);
             next.store(stages[c & 1], rec[c], p);
-            bar_arrive(1 + (c & 1), kThreads);
+            bar_arrive(kFull + (c & 1), kThreads);
             if (c + 1 < used) fetch(c + 1);
         }
-    } else {  // --------------------------------------------------------- sixteen rows of the state a warp
-        const int row = row_base + warp * 16 + (lane >> 2), col2 = 2 * (lane & 3);
-        float w[D / 8][4];
-        float* W = a.W + unit * D * D + (long)row * D + col2;
+    } else if (warp < T::kChain) {  // ---------------------------------- the state: a pair of warps for sixteen rows
+        const int group = warp >> 1, half = warp & 1, tok0 = 32 * half;
+        Exchange<D, NP>& ex = exchanges[group];
+        auto pair = [&] { bar_sync(kPair + group, 64); };
+        const int row = row_base + group * 16 + (lane >> 2);
+        float w[D / 16][4];
+        float* W = a.W + unit * D * D + (long)row * D + half * (D / 2) + col2;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
+        for (int i = 0; i < D / 16; ++i) {
             const float2 u = *reinterpret_cast<const float2*>(W + 8 * i);
             const float2 z = *reinterpret_cast<const float2*>(W + 8 * D + 8 * i);
             w[i][0] = u.x, w[i][1] = u.y, w[i][2] = z.x, w[i][3] = z.y;
@@ -57,147 +74,205 @@ __global__ void __launch_bounds__(RW * 2 + kProducers, 1)
         for (int c = 0; c < used; ++c) {
             S& s = stages[c & 1];
             if constexpr (STATES) {
-                float* o = st.states + ((unit * chunks + c) * D + row) * D + col2;
+                float* o = st.states + ((unit * chunks + c) * D + row) * D + half * (D / 2) + col2;
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
+                for (int i = 0; i < D / 16; ++i) {
                     *reinterpret_cast<float2*>(o + 8 * i) = make_float2(w[i][0], w[i][1]);
                     *reinterpret_cast<float2*>(o + 8 * D + 8 * i) = make_float2(w[i][2], w[i][3]);
                 }
             }
-            bar_sync(1 + (c & 1), kThreads);
-            const uint32_t ks = smem_u32(s.k), qs = smem_u32(s.q), ns = smem_u32(s.n), ps = smem_u32(s.p);
-            const float k_inv = s.scal[2], q_inv = s.scal[3], n_inv = s.scal[4], p_inv = s.scal[5];
-            float* vs = s.v + warp * 16 + (lane >> 2);
-            // W0 K^T and W0 Q^T
-            float x[8][4] = {}, y[STATES ? 1 : 8][4] = {};
-            float i0, i1;  // inverse scales of the two rows
-            {
-                float top0, top1;
-                row_tops<D / 8>(w, top0, top1);
-                const float s0 = pow2_scale(top0, i0), s1 = pow2_scale(top1, i1);
+            bar_sync(kFull + (c & 1), kThreads);
+            const uint32_t ks = smem_u32(s.k), ns = smem_u32(s.n);
+            const float k_inv = s.scal[2], n_inv = s.scal[4];
+            const float* vs = s.v + group * 16 + (lane >> 2);
+            if (!STATES && c > 0) bar_sync(kOutFree + group, 96);
+            float x[4][4];
+            float2 inv;
+            times_tokens<D, NP>(x, w, inv, ks, ex.part, half, lane, pair,
+                                [&](int kt, const uint32_t(&hi)[4], const uint32_t(&lo)[4]) {
+                                    if constexpr (!STATES) {
+                                        ex.w[0][half * (D / 32) + kt][lane] = as_uint4(hi);
+                                        if constexpr (NP == 2) ex.w[NP - 1][half * (D / 32) + kt][lane] = as_uint4(lo);
+                                    }
+                                });
+            if constexpr (!STATES) ex.w_inv[half][lane] = inv;
+            // X^T = V^T - gamma W0 K^T (row: value, column: token) of the own 32 tokens, and beta X
+            float r[4][4];
 #pragma unroll
-                for (int kt = 0; kt < D / 16; ++kt) {
-                    uint32_t hi[4], lo[4];
-                    split_a<D / 8>(w, kt, s0, s1, hi, lo);
-                    auto from = [&](uint32_t tile) {
-                        return [=](uint32_t(&f)[4], int j, int e) { frag_b<D>(f, tile + e * kC * D * 2, j * 16, kt * 16, lane); };
-                    };
-                    mma_row<2, NP, 0, 4>(x, hi, lo, from(ks));
-                    // y is rounded to the tokens' type: 11 bits of W are enough for bf16
-                    if constexpr (!STATES) mma_row<NP, NP, 0, 4>(y, hi, lo, from(qs));
-                }
-            }
-            // X^T = V^T - gamma W0 K^T (row: value, column: token), and Y's share of W0
-            float r[8][4];  // beta X
-#pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                const int tok = 8 * t + col2;
+            for (int t = 0; t < 4; ++t) {
+                const int tok = tok0 + 8 * t + col2;
                 const float2 gm = *reinterpret_cast<const float2*>(s.gamma + tok);
                 const float2 bt = *reinterpret_cast<const float2*>(s.beta + tok);
                 const float* v0 = vs + tok * S::kVLd;
-                x[t][0] = v0[0] - gm.x * k_inv * (x[t][0] * i0);
-                x[t][1] = v0[S::kVLd] - gm.y * k_inv * (x[t][1] * i0);
-                x[t][2] = v0[8] - gm.x * k_inv * (x[t][2] * i1);
-                x[t][3] = v0[S::kVLd + 8] - gm.y * k_inv * (x[t][3] * i1);
+                x[t][0] = v0[0] - gm.x * k_inv * x[t][0];
+                x[t][1] = v0[S::kVLd] - gm.y * k_inv * x[t][1];
+                x[t][2] = v0[8] - gm.x * k_inv * x[t][2];
+                x[t][3] = v0[S::kVLd + 8] - gm.y * k_inv * x[t][3];
                 r[t][0] = bt.x * x[t][0], r[t][1] = bt.y * x[t][1];
                 r[t][2] = bt.x * x[t][2], r[t][3] = bt.y * x[t][3];
-                if constexpr (!STATES) {
-                    y[t][0] *= gm.x * q_inv * i0, y[t][1] *= gm.y * q_inv * i0;
-                    y[t][2] *= gm.x * q_inv * i1, y[t][3] *= gm.y * q_inv * i1;
-                }
             }
-            // eps^T = X^T - (beta X)^T N^T; N is strictly lower: tokens 16 j + .. see those up to them
+            // eps^T = X^T - (beta X)^T N^T: the own tokens' beta X, and for the second half the first half's
             {
-                float top0, top1;
-                row_tops<8>(r, top0, top1);
-                const float s0 = pow2_scale(top0, i0), s1 = pow2_scale(top1, i1);
-                float acc[8][4] = {};
-                unrolled<4>([&](auto kt) {
-                    uint32_t hi[4], lo[4];
-                    split_a<8>(r, kt, s0, s1, hi, lo);
-                    mma_triangle<kt, true, 2, 2>(acc, hi, lo, [&](uint32_t(&f)[4], int j, int e) {
-                        frag_b<kC>(f, ns + e * kC * kC * 2, j * 16, kt * 16, lane);
-                    });
-                });
+                uint32_t hi[2][4], lo[2][4];
+                uint4(&other)[4][32] = reinterpret_cast<uint4(&)[4][32]>(ex.part[1]);
+                float2 r_inv;
+                share(r, hi, lo, r_inv, other, ex.inv, lane, half == 0);
+                float i0 = r_inv.x, i1 = r_inv.y;
+                auto own = [&](uint32_t(&f)[4], int j, int k, int e) {
+                    frag_b<kC>(f, ns + e * kC * kC * 2, tok0 + j * 16, tok0 + k * 16, lane);
+                };
+                float acc[4][4] = {};
+                mma_row<2, 2, 0, 2>(acc, hi[0], lo[0], [&](uint32_t(&f)[4], int j, int e) { own(f, j, 0, e); });
+                mma_row<2, 2, 1, 2>(acc, hi[1], lo[1], [&](uint32_t(&f)[4], int j, int e) { own(f, j, 1, e); });
+                i0 *= n_inv, i1 *= n_inv;
 #pragma unroll
-                for (int t = 0; t < 8; ++t) {
-                    x[t][0] -= acc[t][0] * i0 * n_inv, x[t][1] -= acc[t][1] * i0 * n_inv;
-                    x[t][2] -= acc[t][2] * i1 * n_inv, x[t][3] -= acc[t][3] * i1 * n_inv;
+                for (int t = 0; t < 4; ++t) {
+                    x[t][0] = fmaf(-acc[t][0], i0, x[t][0]), x[t][1] = fmaf(-acc[t][1], i0, x[t][1]);
+                    x[t][2] = fmaf(-acc[t][2], i1, x[t][2]), x[t][3] = fmaf(-acc[t][3], i1, x[t][3]);
+                }
+                pair();
+                if (half == 1) {
+                    shared_by(hi, lo, r_inv, other, ex.inv, lane);
+                    i0 = r_inv.x * n_inv, i1 = r_inv.y * n_inv;
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
+#pragma unroll
+                    for (int kt = 0; kt < 2; ++kt)
+                        mma_row<2, 2, 0, 2>(acc, hi[kt], lo[kt], [&](uint32_t(&f)[4], int j, int e) {
+                            frag_b<kC>(f, ns + e * kC * kC * 2, 32 + j * 16, kt * 16, lane);
+                        });
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        x[t][0] = fmaf(-acc[t][0], i0, x[t][0]), x[t][1] = fmaf(-acc[t][1], i0, x[t][1]);
+                        x[t][2] = fmaf(-acc[t][2], i1, x[t][2]), x[t][3] = fmaf(-acc[t][3], i1, x[t][3]);
+                    }
                 }
             }
             if constexpr (STATES) {
-                float* o = st.eps + ((unit * chunks + c) * kC) * D + row;
+                float* o = st.eps + ((unit * chunks + c) * kC + tok0) * D + row;
 #pragma unroll
-                for (int t = 0; t < 8; ++t)
+                for (int t = 0; t < 4; ++t)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[(long)(8 * t + col2 + (e & 1)) * D + (e >> 1) * 8] = x[t][e];
             }
 #pragma unroll
-            for (int t = 0; t < 8; ++t) {  // E = beta eps
-                const float2 bt = *reinterpret_cast<const float2*>(s.beta + 8 * t + col2);
+            for (int t = 0; t < 4; ++t) {  // E = beta eps, then l E
+                const float2 bt = *reinterpret_cast<const float2*>(s.beta + tok0 + 8 * t + col2);
+                const float2 l = *reinterpret_cast<const float2*>(s.rest + tok0 + 8 * t + col2);
                 x[t][0] *= bt.x, x[t][1] *= bt.y, x[t][2] *= bt.x, x[t][3] *= bt.y;
+                r[t][0] = l.x * x[t][0], r[t][1] = l.y * x[t][1], r[t][2] = l.x * x[t][2], r[t][3] = l.y * x[t][3];
             }
-            if constexpr (!STATES) {  // Y^T += E^T P^T
-                float top0, top1;
-                row_tops<8>(x, top0, top1);
+            if constexpr (!STATES) {
+                float top0, top1, i0, i1;
+                row_tops<4>(x, top0, top1);
                 const float s0 = pow2_scale(top0, i0), s1 = pow2_scale(top1, i1);
-                float acc[8][4] = {};
-                unrolled<4>([&](auto kt) {
-                    uint32_t hi[4], lo[4];
-                    split_a<8>(x, kt, s0, s1, hi, lo);
-                    mma_triangle<kt, true, NP, NP>(acc, hi, lo, [&](uint32_t(&f)[4], int j, int e) {
-                        frag_b<kC>(f, ps + e * kC * kC * 2, j * 16, kt * 16, lane);
-                    });
-                });
 #pragma unroll
-                for (int t = 0; t < 8; ++t) {  // into V's place, whose columns only this warp reads
-                    float* v0 = vs + (8 * t + col2) * S::kVLd;
-                    v0[0] = y[t][0] + acc[t][0] * i0 * p_inv;
-                    v0[S::kVLd] = y[t][1] + acc[t][1] * i0 * p_inv;
-                    v0[8] = y[t][2] + acc[t][2] * i1 * p_inv;
-                    v0[S::kVLd + 8] = y[t][3] + acc[t][3] * i1 * p_inv;
+                for (int kt = 0; kt < 2; ++kt) {
+                    uint32_t hi[4], lo[4];
+                    split_a<4>(x, kt, s0, s1, hi, lo);
+                    ex.e[0][2 * half + kt][lane] = as_uint4(hi);
+                    if constexpr (NP == 2) ex.e[NP - 1][2 * half + kt][lane] = as_uint4(lo);
                 }
+                ex.e_inv[half][lane] = make_float2(i0, i1);
+                bar_arrive(kOutFull + group, 96);
             }
             // W = gamma_C W + (l E)^T K
-#pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                const float2 l = *reinterpret_cast<const float2*>(s.rest + 8 * t + col2);
-                x[t][0] *= l.x, x[t][1] *= l.y, x[t][2] *= l.x, x[t][3] *= l.y;
-            }
-            {
-                float top0, top1;
-                row_tops<8>(x, top0, top1);
-                const float s0 = pow2_scale(top0, i0), s1 = pow2_scale(top1, i1);
-                add_outer<D, NP>(w, s.gamma[kC - 1], x, s0, s1, i0 * k_inv, i1 * k_inv, ks, lane);
-            }
-            if constexpr (!STATES) {  // two lanes a token: 32 or 64 bytes of its row
-                __syncwarp();
-                const long t0 = (long)c * kC;
-                const int n = (int)min((long)kC, len - t0);
-                const long at = (unit * a.T + t0) * D + row_base + warp * 16 + (lane & 1) * 8;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int tok = i * 16 + (lane >> 1);
-                    if (tok >= n) continue;
-                    float o[8];
-                    load8(s.v + tok * S::kVLd + warp * 16 + (lane & 1) * 8, o);
-                    if (a.attn) {
-                        float g[8];
-                        load8(static_cast<const Tok*>(a.attn) + at + (long)tok * D, g);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) o[j] = g[j] / (1.f + expf(-o[j]));
-                    }
-                    store8(static_cast<Tok*>(a.y) + at + (long)tok * D, o);
-                }
-            }
-            if (c + 2 < used) bar_arrive(3 + (c & 1), kThreads);
+            add_outer_both<D, NP>(w, s.gamma[kC - 1], r, k_inv, ex.outer, ex.outer_inv, ks, half, lane, pair);
+            if (c + 2 < used) bar_arrive(kFree + (c & 1), kThreads);
         }
         if constexpr (!STATES) {
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
+            for (int i = 0; i < D / 16; ++i) {
                 *reinterpret_cast<float2*>(W + 8 * i) = make_float2(w[i][0], w[i][1]);
                 *reinterpret_cast<float2*>(W + 8 * D + 8 * i) = make_float2(w[i][2], w[i][3]);
             }
+        }
+    } else if constexpr (!STATES) {  // ---------------------------------- y of sixteen rows
+        const int group = warp - T::kChain;
+        const Exchange<D, NP>& ex = exchanges[group];
+        for (int c = 0; c < used; ++c) {
+            S& s = stages[c & 1];
+            bar_sync(kFull + (c & 1), kThreads);
+            bar_sync(kOutFull + group, 96);
+            const uint32_t qs = smem_u32(s.q), ps = smem_u32(s.p);
+            const float q_inv = s.scal[3], p_inv = s.scal[5];
+            float y[8][4] = {};
+            auto fragments = [&](const uint4(&from)[32], const uint4(&second)[32], uint32_t(&hi)[4], uint32_t(&lo)[4]) {
+                from_uint4(hi, from[lane]);
+                if constexpr (NP == 2) from_uint4(lo, second[lane]);
+            };
+            // gamma W0 Q^T, a half of the columns at a time: each has its scales. bf16: 11 bits of W and E are enough for an
+            // output that is rounded to 8.
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float acc[8][4] = {};
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    const int kt = h * (D / 32) + i;
+                    uint32_t hi[4], lo[4];
+                    fragments(ex.w[0][kt], ex.w[NP - 1][kt], hi, lo);
+                    mma_row<NP, NP, 0, 4>(acc, hi, lo, [&](uint32_t(&f)[4], int j, int e) {
+                        frag_b<D>(f, qs + e * kC * D * 2, j * 16, kt * 16, lane);
+                    });
+                }
+                const float2 inv = ex.w_inv[h][lane];
+#pragma unroll
+                for (int t = 0; t < 8; ++t) {
+                    y[t][0] = fmaf(acc[t][0], inv.x, y[t][0]), y[t][1] = fmaf(acc[t][1], inv.x, y[t][1]);
+                    y[t][2] = fmaf(acc[t][2], inv.y, y[t][2]), y[t][3] = fmaf(acc[t][3], inv.y, y[t][3]);
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                const float2 gm = *reinterpret_cast<const float2*>(s.gamma + 8 * t + col2);
+                y[t][0] *= gm.x * q_inv, y[t][1] *= gm.y * q_inv, y[t][2] *= gm.x * q_inv, y[t][3] *= gm.y * q_inv;
+            }
+            // + E^T P^T, a half of the tokens at a time; token j shows in the tokens from its block of 16 on
+            unrolled<2>([&](auto h) {
+                float acc[8][4] = {};
+                unrolled<2>([&](auto i) {
+                    constexpr int kt = 2 * h + i;
+                    uint32_t hi[4], lo[4];
+                    fragments(ex.e[0][kt], ex.e[NP - 1][kt], hi, lo);
+                    mma_row<NP, NP, kt, 4>(acc, hi, lo, [&](uint32_t(&f)[4], int j, int e) {
+                        frag_b<kC>(f, ps + e * kC * kC * 2, j * 16, kt * 16, lane);
+                    });
+                });
+                const float2 inv = ex.e_inv[h][lane];
+                const float f0 = inv.x * p_inv, f1 = inv.y * p_inv;
+#pragma unroll
+                for (int t = 0; t < 8; ++t) {
+                    y[t][0] = fmaf(acc[t][0], f0, y[t][0]), y[t][1] = fmaf(acc[t][1], f0, y[t][1]);
+                    y[t][2] = fmaf(acc[t][2], f1, y[t][2]), y[t][3] = fmaf(acc[t][3], f1, y[t][3]);
+                }
+            });
+            if (c + 1 < used) bar_arrive(kOutFree + group, 96);
+            // Into V's place, which both chain warps have read, and out from there: two lanes a token, 32 or 64 bytes of its row
+            float* vs = s.v + group * 16;
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                float* v0 = vs + (lane >> 2) + (8 * t + col2) * S::kVLd;
+                v0[0] = y[t][0], v0[S::kVLd] = y[t][1], v0[8] = y[t][2], v0[S::kVLd + 8] = y[t][3];
+            }
+            __syncwarp();
+            const long t0 = (long)c * kC;
+            const int n = (int)min((long)kC, len - t0);
+            const long at = (unit * a.T + t0) * D + row_base + group * 16 + (lane & 1) * 8;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int tok = i * 16 + (lane >> 1);
+                if (tok >= n) continue;
+                float o[8];
+                load8(vs + tok * S::kVLd + (lane & 1) * 8, o);
+                if (a.attn) {
+                    float g[8];
+                    load8(static_cast<const Tok*>(a.attn) + at + (long)tok * D, g);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) o[j] = g[j] / (1.f + expf(-o[j]));
+                }
+                store8(static_cast<Tok*>(a.y) + at + (long)tok * D, o);
+            }
+            if (c + 2 < used) bar_arrive(kFree + (c & 1), kThreads);
         }
     }
     if constexpr (!STATES) {  // nothing is read behind the sequence's end
@@ -209,21 +284,24 @@ __global__ void __launch_bounds__(RW * 2 + kProducers, 1)
 
 template <int D, int RW, typename Tok, bool STATES>
 cudaError_t launch(const DeltaArgs& a, const void* recs, const DeltaStates& states, cudaStream_t st) {
-    constexpr size_t bytes = 2 * sizeof(Stage<D, RW, sizeof(Tok) == 4 ? 2 : 1, sizeof(Tok) == 4 ? 2 : 1>);
-    static_assert(bytes <= 227 * 1024, "two stages fit an SM");
+    constexpr int NP = sizeof(Tok) == 4 ? 2 : 1;
+    constexpr size_t bytes = 2 * sizeof(Stage<D, RW, NP, NP>) + RW / 16 * sizeof(Exchange<D, NP>);
+    static_assert(bytes <= 227 * 1024, "two stages and the exchanges fit an SM");
     auto* kernel = delta_chunks_kernel<D, RW, Tok, STATES>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)((long)a.B * a.H * (D / RW)), RW * 2 + kProducers, bytes, st>>>(
+    kernel<<<(unsigned)((long)a.B * a.H * (D / RW)), Warps<D, RW, STATES>::kThreads, bytes, st>>>(
         a, static_cast<const DeltaChunk*>(recs), (int)((a.T + kC - 1) / kC), states);
     return cudaGetLastError();
 }
 
+// Rows of a CTA: as many as shared memory and the barriers have room for, but 32 at d = 128, where 64 would leave most SMs without a
+// CTA at the 32 units of a wide memory's batch.
 template <bool STATES>
 cudaError_t launch(const DeltaArgs& a, const void* recs, const DeltaStates& s, cudaStream_t st) {
     if (a.d == 64)
-        return a.bf16 ? launch<64, 64, __nv_bfloat16, STATES>(a, recs, s, st) : launch<64, 64, float, STATES>(a, recs, s, st);
-    return a.bf16 ? launch<128, 64, __nv_bfloat16, STATES>(a, recs, s, st) : launch<128, 32, float, STATES>(a, recs, s, st);
+        return a.bf16 ? launch<64, 64, __nv_bfloat16, STATES>(a, recs, s, st) : launch<64, 32, float, STATES>(a, recs, s, st);
+    return a.bf16 ? launch<128, 32, __nv_bfloat16, STATES>(a, recs, s, st) : launch<128, 16, float, STATES>(a, recs, s, st);
 }
 
 }  // namespace

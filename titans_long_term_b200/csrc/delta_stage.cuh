@@ -44,35 +44,102 @@ __device__ __forceinline__ void mma_row(float (&acc)[NT][4], const uint32_t (&hi
         }
     }
 }
-// The same for k-step KT of a lower triangular 64 x 64 tile of B, whose zero blocks are left out: LOWER: n-tiles from
-// the k-step on, else up to it.
-template <int KT, bool LOWER, int NA, int NB, typename Fragment>
-__device__ __forceinline__ void mma_triangle(float (&acc)[8][4], const uint32_t (&hi)[4], const uint32_t (&lo)[4],
-                                             Fragment fragment) {
-    mma_row<NA, NB, LOWER ? KT : 0, LOWER ? 4 : KT + 1>(acc, hi, lo, fragment);
-}
-// w[row][.] = decay w[row][.] + sum over the 64 tokens of t[row][token] B[token][.]; t's two rows are scaled by s0, s1 on the way
-// and the products by i0, i1. B: NB pieces of a [64][D] tile at `tile`.
+// Two warps share sixteen rows of a state: each has half of its columns in registers and, within a chunk, half of the
+// tokens. What they tell one another goes through shared memory in the layout of the registers, a lane to the same lane of
+// the other warp.
+template <int D, int NP>
+struct Exchange {
+    float4 part[2][4][32];  // partial sums over the writer's columns, for the reader's tokens; [1], once read, takes
+                            // fragments of one half of the tokens that the other one needs
+    uint4 outer[2][4][32];  // fragments of the outer product's left side: 2 k-steps x (hi, lo) of each half of the tokens
+    uint4 w[NP][D / 16][32], e[NP][4][32];  // for the output warp: the state's and the writes' fragments
+    float2 inv[32], outer_inv[2][32], w_inv[2][32], e_inv[2][32];  // inverse scales of a lane's two rows
+};
+__device__ __forceinline__ uint4 as_uint4(const uint32_t (&x)[4]) { return make_uint4(x[0], x[1], x[2], x[3]); }
+__device__ __forceinline__ void from_uint4(uint32_t (&x)[4], uint4 u) { x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w; }
+
+// w[row][.] = decay w[row][.] + sum over 32 tokens of t[row][token] B[token][.] for the columns col0 .. of a half: the two k-steps'
+// fragments hi, lo, tokens from tok0 on; the products times f0, f1. B: NB pieces of a [64][D] tile at `tile`.
 template <int D, int NB>
-__device__ __forceinline__ void add_outer(float (&w)[D / 8][4], float decay, const float (&t)[8][4], float s0, float s1,
-                                          float i0, float i1, uint32_t tile, int lane) {
-    uint32_t hi[4][4], lo[4][4];
+__device__ __forceinline__ void add_outer(float (&w)[D / 16][4], float decay, const uint32_t (&hi)[2][4],
+                                          const uint32_t (&lo)[2][4], float f0, float f1, uint32_t tile, int col0,
+                                          int tok0, int lane) {
+    float acc[D / 16][4] = {};
 #pragma unroll
-    for (int kt = 0; kt < 4; ++kt) split_a<8>(t, kt, s0, s1, hi[kt], lo[kt]);
+    for (int kt = 0; kt < 2; ++kt)
+        mma_row<2, NB, 0, D / 32>(acc, hi[kt], lo[kt], [&](uint32_t(&f)[4], int j, int e) {
+            frag_bt<D>(f, tile + e * kC * D * 2, col0 + j * 16, tok0 + kt * 16, lane);
+        });
 #pragma unroll
-    for (int half = 0; half < D / 64; ++half) {
-        float acc[8][4] = {};
+    for (int j = 0; j < D / 16; ++j) {
+        w[j][0] = fmaf(w[j][0], decay, acc[j][0] * f0), w[j][1] = fmaf(w[j][1], decay, acc[j][1] * f0);
+        w[j][2] = fmaf(w[j][2], decay, acc[j][2] * f1), w[j][3] = fmaf(w[j][3], decay, acc[j][3] * f1);
+    }
+}
+// Splits t (the own tokens, 2 k-steps) into fragments hi, lo, which, where it is `needed`, also go to the other warp; inv: their
+// rows' inverse scales.
+__device__ __forceinline__ void share(const float (&t)[4][4], uint32_t (&hi)[2][4], uint32_t (&lo)[2][4], float2& inv,
+                                      uint4 (&to)[4][32], float2 (&to_inv)[32], int lane, bool needed = true) {
+    float top0, top1;
+    row_tops<4>(t, top0, top1);
+    const float s0 = pow2_scale(top0, inv.x), s1 = pow2_scale(top1, inv.y);
 #pragma unroll
-        for (int kt = 0; kt < 4; ++kt)
-            mma_row<2, NB, 0, 4>(acc, hi[kt], lo[kt], [&](uint32_t(&f)[4], int j, int e) {
-                frag_bt<D>(f, tile + e * kC * D * 2, half * 64 + j * 16, kt * 16, lane);
-            });
+    for (int kt = 0; kt < 2; ++kt) {
+        split_a<4>(t, kt, s0, s1, hi[kt], lo[kt]);
+        if (needed) to[2 * kt][lane] = as_uint4(hi[kt]), to[2 * kt + 1][lane] = as_uint4(lo[kt]);
+    }
+    if (needed) to_inv[lane] = inv;
+}
+// What the other warp shared.
+__device__ __forceinline__ void shared_by(uint32_t (&hi)[2][4], uint32_t (&lo)[2][4], float2& inv,
+                                          const uint4 (&from)[4][32], const float2 (&from_inv)[32], int lane) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            float(&u)[4] = w[half * 8 + j];
-            u[0] = fmaf(u[0], decay, acc[j][0] * i0), u[1] = fmaf(u[1], decay, acc[j][1] * i0);
-            u[2] = fmaf(u[2], decay, acc[j][2] * i1), u[3] = fmaf(u[3], decay, acc[j][3] * i1);
-        }
+    for (int kt = 0; kt < 2; ++kt) from_uint4(hi[kt], from[2 * kt][lane]), from_uint4(lo[kt], from[2 * kt + 1][lane]);
+    inv = from_inv[lane];
+}
+// The outer product of both halves of the tokens: this warp's t and, through `ex`, the other one's. `pair` is the two
+// warps' barrier.
+template <int D, int NB, typename Pair>
+__device__ __forceinline__ void add_outer_both(float (&w)[D / 16][4], float decay, const float (&t)[4][4], float factor,
+                                               uint4 (&ex)[2][4][32], float2 (&ex_inv)[2][32], uint32_t tile, int half,
+                                               int lane, Pair pair) {
+    uint32_t hi[2][4], lo[2][4];
+    float2 inv;
+    share(t, hi, lo, inv, ex[half], ex_inv[half], lane);
+    const int col0 = half * (D / 2);
+    add_outer<D, NB>(w, decay, hi, lo, inv.x * factor, inv.y * factor, tile, col0, half * 32, lane);
+    pair();
+    shared_by(hi, lo, inv, ex[half ^ 1], ex_inv[half ^ 1], lane);
+    add_outer<D, NB>(w, 1.f, hi, lo, inv.x * factor, inv.y * factor, tile, col0, 32 - half * 32, lane);
+}
+
+// The state's sixteen rows times the tokens of K (tile): out, the own half of the tokens. inv: inverse scales of this warp's half of
+// the columns; keep(kt, hi, lo) sees the fragments of its k-step kt.
+template <int D, int NP, typename Pair, typename Keep>
+__device__ __forceinline__ void times_tokens(float (&out)[4][4], const float (&w)[D / 16][4], float2& inv, uint32_t tile,
+                                             float4 (&ex)[2][4][32], int half, int lane, Pair pair, Keep keep) {
+    float top0, top1;
+    row_tops<D / 16>(w, top0, top1);
+    const float s0 = pow2_scale(top0, inv.x), s1 = pow2_scale(top1, inv.y);
+    float x[8][4] = {};
+#pragma unroll
+    for (int kt = 0; kt < D / 32; ++kt) {
+        uint32_t hi[4], lo[4];
+        split_a<D / 16>(w, kt, s0, s1, hi, lo);
+        mma_row<2, NP, 0, 4>(x, hi, lo, [&](uint32_t(&f)[4], int j, int e) {  // n-tiles in the order own, other half
+            frag_b<D>(f, tile + e * kC * D * 2, ((j + 2 * half) & 3) * 16, half * (D / 2) + kt * 16, lane);
+        });
+        keep(kt, hi, lo);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        ex[half][i][lane] = make_float4(x[4 + i][0] * inv.x, x[4 + i][1] * inv.x, x[4 + i][2] * inv.y, x[4 + i][3] * inv.y);
+    pair();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 u = ex[half ^ 1][i][lane];
+        out[i][0] = fmaf(x[i][0], inv.x, u.x), out[i][1] = fmaf(x[i][1], inv.x, u.y);
+        out[i][2] = fmaf(x[i][2], inv.y, u.z), out[i][3] = fmaf(x[i][3], inv.y, u.w);
     }
 }
 
