@@ -12,107 +12,114 @@
 // precision also where dk and dq are rounded to bf16: all run on fp16 pieces of 22 bits.
 //
 // One CTA per (key head, chunk) goes through the value heads that share the key head and adds up their dq and dk in
-// registers, in a fixed order. A warp has D/8 columns of dk and dq for all 64 tokens, so that each element of W0
-// and A is loaded by one lane of one warp, straight into the B fragment it belongs to.
+// registers, in a fixed order. A warp has 32 tokens and 16 columns of dk and dq. Everything a product reads lies in shared memory
+// as fp16 pieces, the two states one after the other and 64 rows at a time; each is read from memory twice, first for
+// its largest value and <A, W0>.
 #include "delta_common.cuh"
 
 namespace titans {
 namespace {
 
-constexpr int kThreads = 256;
-
 template <int D, int NP>
 struct Shared {
+    static constexpr int kGroups = D / 16, kWarps = 2 * kGroups;  // column groups; two halves of the tokens each
     __half k[NP][kC * D], q[NP][kC * D], dy[NP][kC * D];
     __half e[2][kC * D], f[2][kC * D];
     __half dp[2][kC * kC], dm[2][kC * kC];
+    union {
+        __half w[2][kC * D];          // 64 rows of W0 or A
+        float part[kGroups][kC];      // dG of a group's columns
+    };
     float gamma[kC], rest[kC], beta[kC], ghi[kC], glo[kC];
     int zeros[kC];
-    float part[8][kC];  // dG of a warp's columns
-    float end[8];       // its share of dG_C
-    float tops[4][8];
+    float sums[kWarps];               // <A, W0>, then dG_C's other part
+    float tops[6][kWarps];
 };
 
-// Largest of a value over the CTA; `slot` of the four in turn so that one call's reads need no barrier of their own
-// before the next call's writes.
-__device__ __forceinline__ float block_max(float x, float (&slot)[8], int warp, int lane) {
-    x = warp_max(x);
-    if (lane == 0) slot[warp] = x;
-    __syncthreads();
-    float t = slot[0];
+template <int WARPS>
+__device__ __forceinline__ float max_of(const float* x) {
+    float t = x[0];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) t = fmaxf(t, slot[i]);
+    for (int i = 1; i < WARPS; ++i) t = fmaxf(t, x[i]);
     return t;
 }
 
-// t (4 x NT tiles of 16 tokens x 8 columns) = rows of A, a tile in shared memory, times B fragments in registers.
-template <int D, int NA, int NT>
-__device__ __forceinline__ void times_state(float (&t)[4][NT][4], uint32_t tile, const uint32_t (&b)[D / 16][NT][2][2],
-                                            int lane) {
-#pragma unroll
-    for (int m = 0; m < 4; ++m)
-#pragma unroll
-        for (int kt = 0; kt < D / 16; ++kt) {
-            uint32_t x[NA][4];
-#pragma unroll
-            for (int e = 0; e < NA; ++e) frag_a<D>(x[e], tile + e * kC * D * 2, m * 16, kt * 16, lane);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) mma_all<NA, 2>(t[m][n], x, b[kt][n]);
-        }
-}
-
-// t += S B (TRANS: S^T B) for a lower triangular tile S [64][64] and the columns n0.. of a tile B [64][D].
-template <int D, int NB, int NT, bool TRANS>
-__device__ __forceinline__ void times_tokens(float (&t)[4][NT][4], uint32_t s, uint32_t tile, int n0, int lane) {
+// a += A B for this warp's 32 tokens of the tile at `left` (NA pieces of [64][LD], 16 steps of k from column k0 on) and its 16 columns of the
+// two-piece tile [64][D] at `right`, rows = k.
+template <int D, int NA>
+__device__ __forceinline__ void times_rows(float (&t)[2][2][4], uint32_t left, int k0, uint32_t right, int m0, int n0, int lane) {
 #pragma unroll
     for (int kt = 0; kt < 4; ++kt) {
-        uint32_t b[NT][NB][2];
+        uint32_t hi[4], lo[4];
+        frag_bt<D>(hi, right, n0, kt * 16, lane);
+        frag_bt<D>(lo, right + kC * D * 2, n0, kt * 16, lane);
 #pragma unroll
-        for (int e = 0; e < NB; ++e) {
-            uint32_t f[4];
-            frag_bt<D>(f, tile + e * kC * D * 2, n0 & ~15, kt * 16, lane);
+        for (int m = 0; m < 2; ++m) {
+            uint32_t x[NA][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const int at = NT == 2 ? 2 * n : (n0 & 8) >> 2;
-                b[n][e][0] = at ? f[2] : f[0], b[n][e][1] = at ? f[3] : f[1];
+            for (int e = 0; e < NA; ++e) frag_a<D>(x[e], left + e * kC * D * 2, m0 + m * 16, k0 + kt * 16, lane);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const uint32_t b[2][2] = {{hi[2 * n], hi[2 * n + 1]}, {lo[2 * n], lo[2 * n + 1]}};
+                mma_all<NA, 2>(t[m][n], x, b);
             }
         }
+    }
+}
+// t += S B (TRANS: S^T B) for a lower triangular two-piece tile S [64][64] and the tile B [64][D] of NB pieces.
+template <int D, int NB, bool TRANS>
+__device__ __forceinline__ void times_tokens(float (&t)[2][2][4], uint32_t s, uint32_t tile, int m0, int n0, int lane) {
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            if (TRANS ? kt < m : kt > m) continue;
+    for (int kt = 0; kt < 4; ++kt) {
+        if (TRANS ? kt * 16 < m0 : kt * 16 > m0 + 16) continue;
+        uint32_t f[NB][4];
+#pragma unroll
+        for (int e = 0; e < NB; ++e) frag_bt<D>(f[e], tile + e * kC * D * 2, n0, kt * 16, lane);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            if (TRANS ? kt * 16 < m0 + m * 16 : kt * 16 > m0 + m * 16) continue;
             uint32_t x[2][4];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 if constexpr (TRANS)
-                    frag_at<kC>(x[e], s + e * kC * kC * 2, m * 16, kt * 16, lane);
+                    frag_at<kC>(x[e], s + e * kC * kC * 2, m0 + m * 16, kt * 16, lane);
                 else
-                    frag_a<kC>(x[e], s + e * kC * kC * 2, m * 16, kt * 16, lane);
+                    frag_a<kC>(x[e], s + e * kC * kC * 2, m0 + m * 16, kt * 16, lane);
             }
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma_all<2, NB>(t[m][n], x, b[n]);
+            for (int n = 0; n < 2; ++n) {
+                uint32_t b[NB][2];
+#pragma unroll
+                for (int e = 0; e < NB; ++e) b[e][0] = f[e][2 * n], b[e][1] = f[e][2 * n + 1];
+                mma_all<2, NB>(t[m][n], x, b);
+            }
         }
     }
 }
 
 template <int D, typename Tok>
-__global__ void __launch_bounds__(kThreads) delta_grads_kernel(DeltaArgs a, const DeltaChunk* recs, int chunks, DeltaGrads g) {
-    constexpr int NP = sizeof(Tok) == 4 ? 2 : 1, NT = D / 64, NC = D / 8, VEC = kC * D / 8 / kThreads;
+__global__ void __launch_bounds__(D * 4, D == 64 ? 2 : 1)
+    delta_grads_kernel(DeltaArgs a, const DeltaChunk* recs, int chunks, DeltaGrads g) {
+    constexpr int NP = sizeof(Tok) == 4 ? 2 : 1, kThreads = D * 4, NC = D / 8, VEC = kC * D / 8 / kThreads;  // VEC = 2
+    constexpr int VW = D * D / 8 / kThreads;  // blocks of eight values of a state a thread
     using S = Shared<D, NP>;
+    constexpr int kWarps = S::kWarps;
     extern __shared__ __align__(1024) unsigned char smem[];
     S& s = *reinterpret_cast<S*>(smem);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n0 = warp * NC, col2 = 2 * (lane & 3);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, col2 = 2 * (lane & 3);
+    const int m0 = (warp & 1) * 32, group = warp >> 1, n0 = group * 16;
     const long key_head = blockIdx.x / chunks, b = key_head / a.Hk;
-    const int chunk = (int)(blockIdx.x % chunks), group = a.H / a.Hk;
+    const int chunk = (int)(blockIdx.x % chunks), heads = a.H / a.Hk;
     const long t0 = (long)chunk * kC, len = delta_length(a, b);
     const int rows = (int)min((long)kC, a.T - t0), n = (int)max(0L, min((long)kC, len - t0));  // tokens there, tokens that count
     const long tok0 = key_head * a.T + t0;
     Tok* dk = static_cast<Tok*>(g.dk) + tok0 * D;
     Tok* dq = static_cast<Tok*>(g.dq) + tok0 * D;
-    const long unit0 = b * a.H + (key_head % a.Hk) * group;
+    const long unit0 = b * a.H + (key_head % a.Hk) * heads;
     if (n == 0) {  // behind the sequence's end: zeros
         const float zero[8] = {};
         for (int i = tid; i < rows * NC; i += kThreads) store8(dk + i * 8, zero), store8(dq + i * 8, zero);
-        for (int h = 0; h < group; ++h) {
+        for (int h = 0; h < heads; ++h) {
             const long at = (unit0 + h) * a.T + t0;
             for (int i = tid; i < rows * NC; i += kThreads) store8(static_cast<Tok*>(g.dv) + at * D + i * 8, zero);
             for (int i = tid; i < rows; i += kThreads) g.dg[at + i] = g.dbeta[at + i] = 0.f;
@@ -120,8 +127,8 @@ __global__ void __launch_bounds__(kThreads) delta_grads_kernel(DeltaArgs a, cons
         return;
     }
     const uint32_t ks = smem_u32(s.k), qs = smem_u32(s.q), ys = smem_u32(s.dy), es = smem_u32(s.e), fs = smem_u32(s.f),
-                   dps = smem_u32(s.dp), dms = smem_u32(s.dm);
-    constexpr uint32_t kTile = kC * D * 2, kPair = kC * kC * 2;
+                   dps = smem_u32(s.dp), dms = smem_u32(s.dm), ws = smem_u32(s.w);
+    constexpr uint32_t kTile = kC * D * 2;
     float k_inv, q_inv;
     {
         const DeltaChunk& r = recs[unit0 * chunks + chunk];
@@ -139,32 +146,45 @@ __global__ void __launch_bounds__(kThreads) delta_grads_kernel(DeltaArgs a, cons
             put8<NP>(qs + swz<D>(row, block % NC), kTile, z, sq);
         }
     }
-    float dq_sum[4][NT][4] = {}, dk_sum[4][NT][4] = {};
-    // Values of K or Q at this lane's places of row tile m and column tile j, rows +0 and +8
-    auto token_at = [&](const __half* tile, float inv, int m, int j, float (&x)[4]) {
+    float dq_sum[2][2][4] = {}, dk_sum[2][2][4] = {};
+    // Values of K or Q at this lane's places
+    auto tokens = [&](const __half* tile, float inv, float(&x)[2][2][4]) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int row = m * 16 + (lane >> 2) + h * 8, at = swz<D>(row, (n0 >> 3) + j) / 2 + col2;
-            float2 v = __half22float2(*reinterpret_cast<const __half2*>(tile + at));
-            if constexpr (NP == 2) {
-                const float2 l = __half22float2(*reinterpret_cast<const __half2*>(tile + kC * D + at));
-                v.x += l.x, v.y += l.y;
-            }
-            x[2 * h] = v.x * inv, x[2 * h + 1] = v.y * inv;
-        }
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int at = swz<D>(m0 + m * 16 + (lane >> 2) + h * 8, (n0 >> 3) + j) / 2 + col2;
+                    float2 v = __half22float2(*reinterpret_cast<const __half2*>(tile + at));
+                    if constexpr (NP == 2) {
+                        const float2 l = __half22float2(*reinterpret_cast<const __half2*>(tile + kC * D + at));
+                        v.x += l.x, v.y += l.y;
+                    }
+                    x[m][j][2 * h] = v.x * inv, x[m][j][2 * h + 1] = v.y * inv;
+                }
+    };
+    auto each = [&](auto f) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f(m, j, e);
     };
 
-    for (int h = 0; h < group; ++h) {
+    for (int h = 0; h < heads; ++h) {
         const long unit = unit0 + h, rec = unit * chunks + chunk, tok = unit * a.T + t0;
         const DeltaChunk& r = recs[rec];
+        const float *w0 = g.fwd.states + rec * D * D, *adj = g.adj + rec * D * D;
         __syncthreads();  // the last head's tiles are no longer read
         if (tid < kC) {
             s.gamma[tid] = r.gamma[tid], s.rest[tid] = r.rest[tid], s.beta[tid] = r.beta[tid];
             s.ghi[tid] = r.ghi[tid], s.glo[tid] = r.glo[tid], s.zeros[tid] = r.zeros[tid];
         }
-        float y_inv, e_inv, f_inv;
-        {  // dY, E and F as pieces; dV and dbeta on the way
-            float y[VEC][8], e[VEC][8], f[VEC][8], top[3] = {0.f, 0.f, 0.f};
+        float y_inv, e_inv, f_inv, w_inv, a_inv, sw, sa, inner;
+        {  // dY, E and F as pieces; dV and dbeta on the way; the states' largest values and <A, W0>
+            float y[VEC][8], e[VEC][8], f[VEC][8], top[5] = {}, dot_wa = 0.f;
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
                 const int block = i * kThreads + tid, row = block / NC;
@@ -176,6 +196,21 @@ __global__ void __launch_bounds__(kThreads) delta_grads_kernel(DeltaArgs a, cons
 #pragma unroll
                     for (int j = 0; j < 8; ++j) y[i][j] = 0.f;
                 }
+            }
+#pragma unroll
+            for (int i = 0; i < VW; ++i) {
+                float x[8], z[8];
+                load8(w0 + (long)(i * kThreads + tid) * 8, x);
+                load8(adj + (long)(i * kThreads + tid) * 8, z);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    top[3] = fmaxf(top[3], fabsf(x[j])), top[4] = fmaxf(top[4], fabsf(z[j]));
+                    dot_wa = fmaf(x[j], z[j], dot_wa);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const int block = i * kThreads + tid, row = block / NC;
                 float dot = 0.f;
                 const float beta = r.beta[row];
 #pragma unroll
@@ -193,9 +228,21 @@ __global__ void __launch_bounds__(kThreads) delta_grads_kernel(DeltaArgs a, cons
                     store8(static_cast<Tok*>(g.dv) + tok * D + (long)block * 8, f[i]);
                 }
             }
-            const float sy = pow2_scale(block_max(top[0], s.tops[0], warp, lane), y_inv);
-            const float se = pow2_scale(block_max(top[1], s.tops[1], warp, lane), e_inv);
-            const float sf = pow2_scale(block_max(top[2], s.tops[2], warp, lane), f_inv);
+#pragma unroll
+            for (int i = 0; i < 5; ++i) {
+                top[i] = warp_max(top[i]);
+                if (lane == 0) s.tops[i][warp] = top[i];
+            }
+#pragma unroll
+            for (int d = 16; d; d >>= 1) dot_wa += __shfl_xor_sync(0xffffffffu, dot_wa, d);
+            if (lane == 0) s.sums[warp] = dot_wa;
+            __syncthreads();
+            const float sy = pow2_scale(max_of<kWarps>(s.tops[0]), y_inv);
+            const float se = pow2_scale(max_of<kWarps>(s.tops[1]), e_inv);
+            const float sf = pow2_scale(max_of<kWarps>(s.tops[2]), f_inv);
+            sw = pow2_scale(max_of<kWarps>(s.tops[3]), w_inv), sa = pow2_scale(max_of<kWarps>(s.tops[4]), a_inv);
+            inner = 0.f;
+            for (int i = 0; i < kWarps; ++i) inner += s.sums[i];
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
                 const int block = i * kThreads + tid;
@@ -205,27 +252,41 @@ __global__ void __launch_bounds__(kThreads) delta_grads_kernel(DeltaArgs a, cons
                 put8<2>(fs + at, kTile, f[i], sf);
             }
         }
+        // 64 rows of a state into the tile w
+        auto stage_state = [&](const float* src, int row0, float sc) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const int block = i * kThreads + tid;
+                float x[8];
+                load8(src + (long)row0 * D + (long)block * 8, x);
+                put8<2>(ws + swz<D>(block / NC, block % NC), kTile, x, sc);
+            }
+        };
+        stage_state(w0, 0, sw);
         __syncthreads();
         float dp_inv, dm_inv;
-        {  // warps 0..3: rows of dP; 4..7: rows of dM
-            const int m0 = (warp & 3) * 16;
-            const bool second = warp >= 4;
-            float t[8][4] = {};
+        {  // rows of dP (even) and of dM (odd pairs of warps), d = 128: half of the columns a warp
+            constexpr int kShare = kWarps / 8;
+            const int r0 = (warp & 3) * 16;
+            const bool second = (warp >> 2) & 1;
+            const int j0 = kShare == 2 ? (warp >> 3) * 2 : 0;
+            float t[8 / kShare][4] = {};
+#pragma unroll 2
             for (int kt = 0; kt < D / 16; ++kt) {
                 uint32_t x[2][4];
                 if (second) {
-                    frag_a<D>(x[0], fs, m0, kt * 16, lane);
-                    frag_a<D>(x[1], fs + kTile, m0, kt * 16, lane);
+                    frag_a<D>(x[0], fs, r0, kt * 16, lane);
+                    frag_a<D>(x[1], fs + kTile, r0, kt * 16, lane);
                 } else {
-                    frag_a<D>(x[0], ys, m0, kt * 16, lane);
-                    if constexpr (NP == 2) frag_a<D>(x[1], ys + kTile, m0, kt * 16, lane);
+                    frag_a<D>(x[0], ys, r0, kt * 16, lane);
+                    if constexpr (NP == 2) frag_a<D>(x[1], ys + kTile, r0, kt * 16, lane);
                 }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (j * 16 > m0) continue;
+                for (int j = 0; j < 4 / kShare; ++j) {
+                    if ((j0 + j) * 16 > r0) continue;
                     uint32_t hi[4], lo[4];
-                    frag_b<D>(hi, es, j * 16, kt * 16, lane);
-                    frag_b<D>(lo, es + kTile, j * 16, kt * 16, lane);
+                    frag_b<D>(hi, es, (j0 + j) * 16, kt * 16, lane);
+                    frag_b<D>(lo, es + kTile, (j0 + j) * 16, kt * 16, lane);
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         mma16816(t[2 * j + q], x[0], hi[2 * q], hi[2 * q + 1]);
@@ -237,156 +298,110 @@ __global__ void __launch_bounds__(kThreads) delta_grads_kernel(DeltaArgs a, cons
             const float inv = e_inv * (second ? -f_inv : y_inv);
             float top = 0.f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < 8 / kShare; ++j) {
+                if ((j0 + j / 2) * 16 > r0) continue;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int row = m0 + (lane >> 2) + (e >> 1) * 8, col = 8 * j + col2 + (e & 1);
+                    const int row = r0 + (lane >> 2) + (e >> 1) * 8, col = j0 * 16 + 8 * j + col2 + (e & 1);
                     t[j][e] = (second ? col < row : col <= row)
                                   ? t[j][e] * inv * decay_between(s.ghi, s.glo, s.zeros, row, col)
                                   : 0.f;
                     top = fmaxf(top, fabsf(t[j][e]));
                 }
+            }
             top = warp_max(top);
-            if (lane == 0) s.tops[3][warp] = top;
+            if (lane == 0) s.tops[5][warp] = top;
             __syncthreads();
-            const float(&w)[8] = s.tops[3];
-            const float sp = pow2_scale(fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3])), dp_inv);
-            const float sm = pow2_scale(fmaxf(fmaxf(w[4], w[5]), fmaxf(w[6], w[7])), dm_inv);
-            const float sc = second ? sm : sp;
+            float tp = 0.f, tm = 0.f;
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) {
+                if (i & 4)
+                    tm = fmaxf(tm, s.tops[5][i]);
+                else
+                    tp = fmaxf(tp, s.tops[5][i]);
+            }
+            const float sp = pow2_scale(tp, dp_inv), sm = pow2_scale(tm, dm_inv), sc = second ? sm : sp;
             unsigned char* dst = reinterpret_cast<unsigned char*>(second ? s.dm : s.dp);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < 8 / kShare; ++j) {
+                if ((j0 + j / 2) * 16 > r0) continue;  // only the lower blocks are read
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     uint32_t hi, lo;
                     split2(t[j][2 * q] * sc, t[j][2 * q + 1] * sc, hi, lo);
-                    const uint32_t at = swz<kC>(m0 + (lane >> 2) + q * 8, j) + (lane & 3) * 4;
+                    const uint32_t at = swz<kC>(r0 + (lane >> 2) + q * 8, j0 * 2 + j) + (lane & 3) * 4;
                     *reinterpret_cast<uint32_t*>(dst + at) = hi;
-                    *reinterpret_cast<uint32_t*>(dst + kPair + at) = lo;
+                    *reinterpret_cast<uint32_t*>(dst + kC * kC * 2 + at) = lo;
                 }
+            }
         }
         __syncthreads();
-        float dG[4][2] = {};  // of rows 16 m + lane / 4, + 8
-        // adds t to `sum`, and its products with the token (sign) to dG; returns their total
-        auto take = [&](float(&t)[4][NT][4], float(&sum)[4][NT][4], const __half* tile, float inv, float sign) {
-            float total = 0.f;
+        float dG[2][2] = {};  // of rows m0 + 16 m + lane / 4, + 8
+        auto by_row = [&](const float* x, int m, int e) { return x[m0 + m * 16 + (lane >> 2) + (e >> 1) * 8]; };
+        float u[2][2][4] = {};
+        {  // dQ = gamma dY W0 + dP K, and the reading role of k: u = -gamma F W0 + dM K
+            float t[2][2][4] = {}, acc[2][2][4] = {}, x[2][2][4];
 #pragma unroll
-            for (int m = 0; m < 4; ++m)
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    float x[4];
-                    token_at(tile, inv, m, j, x);
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const float d = t[m][j][2 * q] * x[2 * q] + t[m][j][2 * q + 1] * x[2 * q + 1];
-                        dG[m][q] = fmaf(sign, d, dG[m][q]);
-                        total += d;
-                    }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sum[m][j][e] += t[m][j][e];
+            for (int part = 0; part < D / 64; ++part) {
+                if (part > 0) {
+                    __syncthreads();
+                    stage_state(w0, part * 64, sw);
+                    __syncthreads();
                 }
-            return total;
-        };
-        auto scale_rows = [&](float(&t)[4][NT][4], const float* by, float f) {
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const float f0 = by[m * 16 + (lane >> 2)] * f, f1 = by[m * 16 + (lane >> 2) + 8] * f;
-#pragma unroll
-                for (int j = 0; j < NT; ++j) t[m][j][0] *= f0, t[m][j][1] *= f0, t[m][j][2] *= f1, t[m][j][3] *= f1;
+                times_rows<D, NP>(t, ys, part * 64, ws, m0, n0, lane);
+                times_rows<D, 2>(u, fs, part * 64, ws, m0, n0, lane);
             }
-        };
-        auto add_scaled = [&](float(&t)[4][NT][4], const float(&u)[4][NT][4], float f) {
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) t[m][j][e] = fmaf(u[m][j][e], f, t[m][j][e]);
-        };
-        // This lane's elements of W0 and A: rows 16 kt + 2 (lane % 4) + {0, 1, 8, 9}, columns n0 + 8 j + lane / 4
-        float w0[D / 16][NT][4];
-        uint32_t wb[D / 16][NT][2][2];
-        float w_inv, end = 0.f;
-        auto load_state = [&](const float* src, float(&x)[D / 16][NT][4]) {
-            float top = 0.f;
-#pragma unroll
-            for (int kt = 0; kt < D / 16; ++kt)
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        x[kt][j][e] = src[(kt * 16 + col2 + (e & 1) + (e >> 1) * 8) * D + n0 + 8 * j + (lane >> 2)];
-                        top = fmaxf(top, fabsf(x[kt][j][e]));
-                    }
-            return warp_max(top);
-        };
-        auto to_pieces = [&](const float(&x)[D / 16][NT][4], float sc) {
-#pragma unroll
-            for (int kt = 0; kt < D / 16; ++kt)
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int q = 0; q < 2; ++q)
-                        split2(x[kt][j][2 * q] * sc, x[kt][j][2 * q + 1] * sc, wb[kt][j][0][q], wb[kt][j][1][q]);
-        };
-        to_pieces(w0, pow2_scale(load_state(g.fwd.states + rec * D * D, w0), w_inv));
-        {  // dQ = gamma dY W0 + dP K
-            float t[4][NT][4] = {}, u[4][NT][4] = {};
-            times_state<D, NP, NT>(t, ys, wb, lane);
-            scale_rows(t, s.gamma, y_inv * w_inv);
-            times_tokens<D, NP, NT, false>(u, dps, ks, n0, lane);
-            add_scaled(t, u, dp_inv * k_inv);
-            take(t, dq_sum, s.q[0], q_inv, 1.f);
+            times_tokens<D, NP, false>(acc, dps, ks, m0, n0, lane);
+            tokens(s.q[0], q_inv, x);
+            each([&](int m, int j, int e) {
+                const float v = fmaf(t[m][j][e], by_row(s.gamma, m, e) * (y_inv * w_inv), acc[m][j][e] * (dp_inv * k_inv));
+                dq_sum[m][j][e] += v;
+                dG[m][e >> 1] = fmaf(v, x[m][j][e], dG[m][e >> 1]);
+                acc[m][j][e] = 0.f;
+            });
+            times_tokens<D, NP, false>(acc, dms, ks, m0, n0, lane);
+            each([&](int m, int j, int e) {
+                u[m][j][e] = fmaf(u[m][j][e], by_row(s.gamma, m, e) * (-f_inv * w_inv), acc[m][j][e] * (dm_inv * k_inv));
+            });
         }
-        {  // dKq = -gamma F W0 + dM K
-            float t[4][NT][4] = {}, u[4][NT][4] = {};
-            times_state<D, 2, NT>(t, fs, wb, lane);
-            scale_rows(t, s.gamma, -f_inv * w_inv);
-            times_tokens<D, NP, NT, false>(u, dms, ks, n0, lane);
-            add_scaled(t, u, dm_inv * k_inv);
-            take(t, dk_sum, s.k[0], k_inv, 1.f);
+        float end = 0.f;
+        {  // the writing role of k: v = l E A + dP^T Q + dM^T K
+            float v[2][2][4] = {}, acc[2][2][4] = {}, x[2][2][4];
+#pragma unroll
+            for (int part = 0; part < D / 64; ++part) {
+                __syncthreads();
+                stage_state(adj, part * 64, sa);
+                __syncthreads();
+                times_rows<D, 2>(v, es, part * 64, ws, m0, n0, lane);
+            }
+            tokens(s.k[0], k_inv, x);
+            times_tokens<D, NP, true>(acc, dps, qs, m0, n0, lane);
+            each([&](int m, int j, int e) {
+                v[m][j][e] *= by_row(s.rest, m, e) * (e_inv * a_inv);
+                end = fmaf(v[m][j][e], x[m][j][e], end);
+                v[m][j][e] = fmaf(acc[m][j][e], dp_inv * q_inv, v[m][j][e]);
+                acc[m][j][e] = 0.f;
+            });
+            times_tokens<D, NP, true>(acc, dms, ks, m0, n0, lane);
+            each([&](int m, int j, int e) {
+                const float z = fmaf(acc[m][j][e], dm_inv * k_inv, v[m][j][e]);
+                dk_sum[m][j][e] += u[m][j][e] + z;
+                dG[m][e >> 1] = fmaf(u[m][j][e] - z, x[m][j][e], dG[m][e >> 1]);
+            });
         }
-        {  // l E A, and gamma_C <A, W0> with W0 put together again from its pieces
-            float dot = 0.f;
-            const float top = load_state(g.adj + rec * D * D, w0);
+        __syncthreads();  // w is free: part takes its place
 #pragma unroll
-            for (int kt = 0; kt < D / 16; ++kt)
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&wb[kt][j][0][q]));
-                        const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&wb[kt][j][1][q]));
-                        dot = fmaf(w0[kt][j][2 * q], (hi.x + lo.x) * w_inv, dot);
-                        dot = fmaf(w0[kt][j][2 * q + 1], (hi.y + lo.y) * w_inv, dot);
-                    }
-            end = dot * s.gamma[kC - 1];
-            to_pieces(w0, pow2_scale(top, w_inv));
-            float t[4][NT][4] = {};
-            times_state<D, 2, NT>(t, es, wb, lane);
-            scale_rows(t, s.rest, e_inv * w_inv);
-            end += take(t, dk_sum, s.k[0], k_inv, -1.f);
-        }
-        {  // dP^T Q + dM^T K
-            float t[4][NT][4] = {}, u[4][NT][4] = {}, zero[4][NT][4] = {};
-            times_tokens<D, NP, NT, true>(u, dps, qs, n0, lane);
-            add_scaled(t, u, dp_inv * q_inv);
-            times_tokens<D, NP, NT, true>(zero, dms, ks, n0, lane);
-            add_scaled(t, zero, dm_inv * k_inv);
-            take(t, dk_sum, s.k[0], k_inv, -1.f);
-        }
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 float x = dG[m][q];
                 x += __shfl_xor_sync(0xffffffffu, x, 1);
                 x += __shfl_xor_sync(0xffffffffu, x, 2);
-                if ((lane & 3) == 0) s.part[warp][m * 16 + (lane >> 2) + q * 8] = x;
+                if ((lane & 3) == 0) s.part[group][m0 + m * 16 + (lane >> 2) + q * 8] = x;
             }
 #pragma unroll
         for (int d = 16; d; d >>= 1) end += __shfl_xor_sync(0xffffffffu, end, d);
-        if (lane == 0) s.end[warp] = end;
+        if (lane == 0) s.sums[warp] = end;
         __syncthreads();
         if (warp == 0) {  // dg_t: the sum of dG from t on, taken from the end, two tokens a lane
             double x[2];
@@ -395,7 +410,11 @@ __global__ void __launch_bounds__(kThreads) delta_grads_kernel(DeltaArgs a, cons
                 const int t = kC - 1 - (2 * lane + i);
                 x[i] = 0.;
 #pragma unroll
-                for (int w = 0; w < 8; ++w) x[i] += s.part[w][t] + (t == kC - 1 ? s.end[w] : 0.f);
+                for (int w = 0; w < S::kGroups; ++w) x[i] += s.part[w][t];
+                if (t == kC - 1) {
+                    x[i] += (double)inner * s.gamma[kC - 1];
+                    for (int w = 0; w < kWarps; ++w) x[i] += s.sums[w];
+                }
             }
             const double sum = warp_prefix(x[0] + x[1], lane);
 #pragma unroll
@@ -406,13 +425,13 @@ __global__ void __launch_bounds__(kThreads) delta_grads_kernel(DeltaArgs a, cons
         }
     }
 #pragma unroll
-    for (int m = 0; m < 4; ++m)
+    for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            const int row = m * 16 + (lane >> 2) + q * 8;
+            const int row = m0 + m * 16 + (lane >> 2) + q * 8;
             if (row >= rows) continue;
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
+            for (int j = 0; j < 2; ++j) {
                 const int at = row * D + n0 + 8 * j + col2;
                 if constexpr (sizeof(Tok) == 4) {
                     *reinterpret_cast<float2*>(dq + at) = make_float2(dq_sum[m][j][2 * q], dq_sum[m][j][2 * q + 1]);
@@ -433,7 +452,7 @@ cudaError_t launch(const DeltaArgs& a, const void* recs, const DeltaGrads& g, cu
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
     const int chunks = (int)((a.T + kC - 1) / kC);
-    kernel<<<(unsigned)((long)a.B * a.Hk * chunks), kThreads, bytes, st>>>(a, static_cast<const DeltaChunk*>(recs), chunks, g);
+    kernel<<<(unsigned)((long)a.B * a.Hk * chunks), D * 4, bytes, st>>>(a, static_cast<const DeltaChunk*>(recs), chunks, g);
     return cudaGetLastError();
 }
 
