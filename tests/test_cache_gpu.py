@@ -238,7 +238,7 @@ def test_binding_refuses_tensors():
         with pytest.raises(TitansError) as e:
             p.cache.attend(q, p.pages, p.table, starts, **bad)
         assert e.value.status == mem.EINVAL
-    with pytest.raises(TitansError):
+    with pytest.raises(ValueError):
         p.cache.read(p.pages, p.table, starts, 0)
 
 

@@ -7,7 +7,7 @@ from typing import Dict, Optional, Tuple
 
 import torch
 
-from .delta import _device, _need, _On
+from .delta import _F32, _I32, _need, _On, _run
 from .mem import CacheConfig, CachePages, _check, lib
 
 TYPES = {"bf16": (0, torch.bfloat16), "e4m3": (1, torch.float8_e4m3fn)}
@@ -33,7 +33,10 @@ class PagedCache:
         h = ctypes.c_void_p()
         _check(lib().titans_cache_init(ctypes.byref(self._cfg), ctypes.byref(h)))
         self._h = h
-        self.device = torch.device("cuda", torch.cuda.current_device())
+        self._lib = lib()
+        self._index = torch.cuda.current_device()
+        self.device = torch.device("cuda", self._index)
+        self._pool, self._table, self._batch = (num_pages, self.kv_heads, page, d), (B, max_pages), (B,)
 
     def close(self):
         if getattr(self, "_h", None):
@@ -57,43 +60,43 @@ class PagedCache:
         return p
 
     def _where(self, pages, table, starts, counts) -> CachePages:
-        shape, dev = (self.num_pages, self.kv_heads, self.page, self.d), self.device
-        for n in ("k", "v"):
-            _need(f"pages {n}", pages[n], self.dtype, shape, dev)
-            if self.scaled:
-                _need(f"pages {n}_scale", pages[n + "_scale"], torch.float32, shape[:-1], dev)
-        _need("table", table, torch.int32, (self.B, self.max_pages), dev)
-        _need("starts", starts, torch.int32, (self.B,), dev)
+        k, v = pages["k"], pages["v"]
+        _need(self._index, ("pages k", k, self.dtype, self._pool), ("pages v", v, self.dtype, self._pool),
+              ("table", table, _I32, self._table), ("starts", starts, _I32, self._batch))
         if counts is not None:
-            _need("counts", counts, torch.int32, (self.B,), dev)
-        p = CachePages(pages["k"].data_ptr(), pages["v"].data_ptr())
-        if self.scaled:
-            p.k_scale, p.v_scale = pages["k_scale"].data_ptr(), pages["v_scale"].data_ptr()
-        return p
+            _need(self._index, ("counts", counts, _I32, self._batch))
+        if not self.scaled:
+            return CachePages(k.data_ptr(), v.data_ptr())
+        ks, vs = pages["k_scale"], pages["v_scale"]
+        _need(self._index, ("pages k_scale", ks, _F32, self._pool[:-1]), ("pages v_scale", vs, _F32, self._pool[:-1]))
+        return CachePages(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr())
 
     def append(self, k, v, pages: Dict[str, torch.Tensor], table, starts, counts: Optional[torch.Tensor] = None,
                stream=None) -> None:
         """Writes k, v [B, kv_heads, T, d] bf16 at positions starts[b] + t, t < counts[b] (None: all T)."""
         T, shape = k.shape[-2], (self.B, self.kv_heads, k.shape[-2], self.d)
-        _need("k", k, torch.bfloat16, shape, self.device)
-        _need("v", v, torch.bfloat16, shape, self.device)
+        _need(self._index, ("k", k, torch.bfloat16, shape), ("v", v, torch.bfloat16, shape))
         p = self._where(pages, table, starts, counts)
-        with _On(self.device, stream) as st:
-            _check(lib().titans_cache_append(self._h, k.data_ptr(), v.data_ptr(), T, ctypes.byref(p),
-                                             table.data_ptr(), starts.data_ptr(),
-                                             None if counts is None else counts.data_ptr(), st))
+        _run(self._index, stream, lambda st: _check(self._lib.titans_cache_append(
+            self._h, k.data_ptr(), v.data_ptr(), T, ctypes.byref(p), table.data_ptr(), starts.data_ptr(),
+            None if counts is None else counts.data_ptr(), st)))
 
     def read(self, pages: Dict[str, torch.Tensor], table, starts, T: int, counts: Optional[torch.Tensor] = None,
              stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
         """k, v [B, kv_heads, T, d] bf16 of positions starts[b] + t; zeros for t >= counts[b]."""
+        if T < 1:
+            raise ValueError(f"T: expected at least 1, got {T}")
         p = self._where(pages, table, starts, counts)
-        with _On(self.device, stream) as st:
-            k, v = (torch.empty(self.B, self.kv_heads, T, self.d, dtype=torch.bfloat16, device=self.device)
-                    for _ in range(2))
-            _check(lib().titans_cache_read(self._h, ctypes.byref(p), table.data_ptr(), starts.data_ptr(),
-                                           None if counts is None else counts.data_ptr(), T, k.data_ptr(),
-                                           v.data_ptr(), st))
-        return k, v
+
+        def call(st):
+            both = torch.empty(2, self.B, self.kv_heads, T, self.d, dtype=torch.bfloat16, device=self.device)
+            k, v = both.unbind()
+            _check(self._lib.titans_cache_read(self._h, ctypes.byref(p), table.data_ptr(), starts.data_ptr(),
+                                               None if counts is None else counts.data_ptr(), T, k.data_ptr(),
+                                               v.data_ptr(), st))
+            return k, v
+
+        return _run(self._index, stream, call)
 
     def attend(self, q, pages: Dict[str, torch.Tensor], table, starts, counts: Optional[torch.Tensor] = None,
                window: int = 0, sinks: int = 0, scale: Optional[float] = None, o: Optional[torch.Tensor] = None,
@@ -102,25 +105,27 @@ class PagedCache:
         `window` > 0 only those with j > p - window or j < sinks; scale defaults to d^-1/2. Rows t >= counts[b]
         are zeros. Returns o [B, H, T, d] bf16, ready to be the `attn` of a gated memory."""
         T, shape = q.shape[-2], (self.B, self.H, q.shape[-2], self.d)
-        _need("q", q, torch.bfloat16, shape, self.device)
+        _need(self._index, ("q", q, torch.bfloat16, shape))
+        if o is not None:
+            _need(self._index, ("o", o, torch.bfloat16, shape))
         p = self._where(pages, table, starts, counts)
-        with _On(self.device, stream) as st:
-            if o is None:
-                o = torch.empty_like(q)
-            else:
-                _need("o", o, torch.bfloat16, shape, self.device)
-            n = self._bytes.get(T)
-            if n is None:
-                n = self._bytes[T] = lib().titans_cache_attend_workspace_bytes(self._h, T)
+        n = self._bytes.get(T)
+        if n is None:
+            n = self._bytes[T] = self._lib.titans_cache_attend_workspace_bytes(self._h, T)
+
+        def call(st):
+            out = torch.empty_like(q) if o is None else o
             ws = torch.empty(n, dtype=torch.uint8, device=self.device) if n else None
-            _check(lib().titans_cache_attend(
+            _check(self._lib.titans_cache_attend(
                 self._h, q.data_ptr(), T, ctypes.byref(p), table.data_ptr(), starts.data_ptr(),
                 None if counts is None else counts.data_ptr(), window, sinks,
-                1.0 / math.sqrt(self.d) if scale is None else scale, o.data_ptr(),
+                1.0 / math.sqrt(self.d) if scale is None else scale, out.data_ptr(),
                 None if ws is None else ws.data_ptr(), n, st))
-        return o
+            return out
+
+        return _run(self._index, stream, call)
 
     def sync_status(self, stream=None):
         """Waits for the stream; raises TitansError if a call met a missing page since the last one."""
-        with _On(self.device, stream) as st:
-            _check(lib().titans_cache_sync_status(self._h, st))
+        with _On(self._index, stream) as st:
+            _check(self._lib.titans_cache_sync_status(self._h, st))
