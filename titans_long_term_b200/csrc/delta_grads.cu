@@ -30,8 +30,9 @@ struct Shared {
         __half w[2][kC * D];          // 64 rows of W0 or A
         float part[kGroups][kC];      // dG of a group's columns
     };
-    float gamma[kC], rest[kC], beta[kC], ghi[kC], glo[kC];
+    float gamma[kC], rest[kC], ghi[kC], glo[kC];
     int zeros[kC];
+    float from[kC], to[3][48];
     float sums[kWarps];               // <A, W0>, then dG_C's other part
     float tops[6][kWarps];
 };
@@ -179,9 +180,10 @@ __global__ void __launch_bounds__(D * 4, D == 64 ? 2 : 1)
         const float *w0 = g.fwd.states + rec * D * D, *adj = g.adj + rec * D * D;
         __syncthreads();  // the last head's tiles are no longer read
         if (tid < kC) {
-            s.gamma[tid] = r.gamma[tid], s.rest[tid] = r.rest[tid], s.beta[tid] = r.beta[tid];
+            s.gamma[tid] = r.gamma[tid], s.rest[tid] = r.rest[tid], s.from[tid] = r.from[tid];
             s.ghi[tid] = r.ghi[tid], s.glo[tid] = r.glo[tid], s.zeros[tid] = r.zeros[tid];
         }
+        if (tid < 144) s.to[0][tid] = r.to[0][tid];
         float y_inv, e_inv, f_inv, w_inv, a_inv, sw, sa, inner;
         {  // dY, E and F as pieces; dV and dbeta on the way; the states' largest values and <A, W0>
             float y[VEC][8], e[VEC][8], f[VEC][8], top[5] = {}, dot_wa = 0.f;
@@ -303,9 +305,10 @@ __global__ void __launch_bounds__(D * 4, D == 64 ? 2 : 1)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int row = r0 + (lane >> 2) + (e >> 1) * 8, col = j0 * 16 + 8 * j + col2 + (e & 1);
-                    t[j][e] = (second ? col < row : col <= row)
-                                  ? t[j][e] * inv * decay_between(s.ghi, s.glo, s.zeros, row, col)
-                                  : 0.f;
+                    const float d = (j0 + j / 2) * 16 < r0              ? s.from[row] * s.to[(warp & 3) - 1][col]
+                                    : (second ? col < row : col <= row) ? decay_between(s.ghi, s.glo, s.zeros, row, col)
+                                                                        : 0.f;
+                    t[j][e] *= inv * d;
                     top = fmaxf(top, fabsf(t[j][e]));
                 }
             }

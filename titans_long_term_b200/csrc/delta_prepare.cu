@@ -29,8 +29,7 @@ struct Common {
     float t_inv[4];
     float beta[kC], ghi[kC], glo[kC];
     int zeros[kC];    // tokens of the chunk so far whose decay is 0
-    float from[kC];   // decay from the end of the block of 16 before token i's to i
-    float to[3][48];  // and from token j to the end of blocks 0, 1 and 2
+    float from[kC], to[3][48];  // as in DeltaChunk
     float tops[16];
 };
 
@@ -176,10 +175,10 @@ __global__ void __launch_bounds__(kThreads, D == 64 && sizeof(Tok) == 2 ? 5 : 3)
     // The decays between blocks, one or two a thread
     for (int x = tid; x < kC + 96; x += kThreads) {
         if (x < kC) {
-            c.from[x] = x < 16 ? 0.f : decay_between(c.ghi, c.glo, c.zeros, x, (x & ~15) - 1);
+            o.from[x] = c.from[x] = x < 16 ? 0.f : decay_between(c.ghi, c.glo, c.zeros, x, (x & ~15) - 1);
         } else {
             const int y = x - kC, block = y < 16 ? 0 : y < 48 ? 1 : 2, j = y - (block == 0 ? 0 : block == 1 ? 16 : 48);
-            c.to[block][j] = decay_between(c.ghi, c.glo, c.zeros, block * 16 + 15, j);
+            o.to[block][j] = c.to[block][j] = decay_between(c.ghi, c.glo, c.zeros, block * 16 + 15, j);
         }
     }
     __syncthreads();
