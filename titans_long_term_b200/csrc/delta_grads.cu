@@ -37,6 +37,9 @@ struct Shared {
     float tops[6][kWarps];
 };
 
+// Row of the i-th of ten lower blocks, which go row by row.
+__device__ __forceinline__ int block_row(int i) { return (i >= 1) + (i >= 3) + (i >= 6); }
+
 template <int WARPS>
 __device__ __forceinline__ float max_of(const float* x) {
     float t = x[0];
@@ -183,7 +186,7 @@ __global__ void __launch_bounds__(D * 4, D == 64 ? 2 : 1)
             s.gamma[tid] = r.gamma[tid], s.rest[tid] = r.rest[tid], s.from[tid] = r.from[tid];
             s.ghi[tid] = r.ghi[tid], s.glo[tid] = r.glo[tid], s.zeros[tid] = r.zeros[tid];
         }
-        if (tid < 144) s.to[0][tid] = r.to[0][tid];
+        if (tid < 144) (&s.to[0][0])[tid] = (&r.to[0][0])[tid];
         float y_inv, e_inv, f_inv, w_inv, a_inv, sw, sa, inner;
         {  // dY, E and F as pieces; dV and dbeta on the way; the states' largest values and <A, W0>
             float y[VEC][8], e[VEC][8], f[VEC][8], top[5] = {}, dot_wa = 0.f;
@@ -267,50 +270,52 @@ __global__ void __launch_bounds__(D * 4, D == 64 ? 2 : 1)
         stage_state(w0, 0, sw);
         __syncthreads();
         float dp_inv, dm_inv;
-        {  // rows of dP (even) and of dM (odd pairs of warps), d = 128: half of the columns a warp
-            constexpr int kShare = kWarps / 8;
-            const int r0 = (warp & 3) * 16;
-            const bool second = (warp >> 2) & 1;
-            const int j0 = kShare == 2 ? (warp >> 3) * 2 : 0;
-            float t[8 / kShare][4] = {};
-#pragma unroll 2
-            for (int kt = 0; kt < D / 16; ++kt) {
-                uint32_t x[2][4];
-                if (second) {
-                    frag_a<D>(x[0], fs, r0, kt * 16, lane);
-                    frag_a<D>(x[1], fs + kTile, r0, kt * 16, lane);
-                } else {
-                    frag_a<D>(x[0], ys, r0, kt * 16, lane);
-                    if constexpr (NP == 2) frag_a<D>(x[1], ys + kTile, r0, kt * 16, lane);
-                }
+        {  // the ten lower 16 x 16 blocks of dP (warps w with w & 4 = 0) and of dM, shared out over their warps
+            constexpr int kTeam = kWarps / 2, kMost = (10 + kTeam - 1) / kTeam;
+            const bool second = warp & 4;
+            const int member = (warp & 3) + (warp >> 3) * 4;
+            float t[kMost][2][4] = {}, top = 0.f;
 #pragma unroll
-                for (int j = 0; j < 4 / kShare; ++j) {
-                    if ((j0 + j) * 16 > r0) continue;
-                    uint32_t hi[4], lo[4];
-                    frag_b<D>(hi, es, (j0 + j) * 16, kt * 16, lane);
-                    frag_b<D>(lo, es + kTile, (j0 + j) * 16, kt * 16, lane);
+            for (int i = 0; i < kMost; ++i) {
+                const int at = member + i * kTeam, br = block_row(at), bc = at - br * (br + 1) / 2;
+                if (at >= 10) continue;
+#pragma unroll 4
+                for (int kt = 0; kt < D / 16; ++kt) {
+                    uint32_t x[2][4], hi[4], lo[4];
+                    frag_a<D>(x[0], second ? fs : ys, br * 16, kt * 16, lane);
+                    if (NP == 2 || second) frag_a<D>(x[1], (second ? fs : ys) + kTile, br * 16, kt * 16, lane);
+                    frag_b<D>(hi, es, bc * 16, kt * 16, lane);
+                    frag_b<D>(lo, es + kTile, bc * 16, kt * 16, lane);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) mma16816(t[i][q], x[0], hi[2 * q], hi[2 * q + 1]);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) mma16816(t[i][q], x[0], lo[2 * q], lo[2 * q + 1]);
+                    if (NP == 2 || second)
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) mma16816(t[i][q], x[1], hi[2 * q], hi[2 * q + 1]);
+                }
+                const float inv = e_inv * (second ? -f_inv : y_inv);
+                const int row = br * 16 + (lane >> 2);
+                if (bc < br) {
+                    const float f0 = s.from[row] * inv, f1 = s.from[row + 8] * inv;
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
-                        mma16816(t[2 * j + q], x[0], hi[2 * q], hi[2 * q + 1]);
-                        mma16816(t[2 * j + q], x[0], lo[2 * q], lo[2 * q + 1]);
-                        if (NP == 2 || second) mma16816(t[2 * j + q], x[1], hi[2 * q], hi[2 * q + 1]);
+                        const float2 to = *reinterpret_cast<const float2*>(&s.to[br - 1][bc * 16 + 8 * q + col2]);
+                        t[i][q][0] *= f0 * to.x, t[i][q][1] *= f0 * to.y, t[i][q][2] *= f1 * to.x, t[i][q][3] *= f1 * to.y;
                     }
-                }
-            }
-            const float inv = e_inv * (second ? -f_inv : y_inv);
-            float top = 0.f;
+                } else {
 #pragma unroll
-            for (int j = 0; j < 8 / kShare; ++j) {
-                if ((j0 + j / 2) * 16 > r0) continue;
+                    for (int q = 0; q < 2; ++q)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int row = r0 + (lane >> 2) + (e >> 1) * 8, col = j0 * 16 + 8 * j + col2 + (e & 1);
-                    const float d = (j0 + j / 2) * 16 < r0              ? s.from[row] * s.to[(warp & 3) - 1][col]
-                                    : (second ? col < row : col <= row) ? decay_between(s.ghi, s.glo, s.zeros, row, col)
-                                                                        : 0.f;
-                    t[j][e] *= inv * d;
-                    top = fmaxf(top, fabsf(t[j][e]));
+                        for (int e = 0; e < 4; ++e) {
+                            const int rr = row + (e >> 1) * 8, cc = bc * 16 + 8 * q + col2 + (e & 1);
+                            t[i][q][e] *= (second ? cc < rr : cc <= rr) ? inv * decay_between(s.ghi, s.glo, s.zeros, rr, cc) : 0.f;
+                        }
                 }
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(t[i][q][e]));
             }
             top = warp_max(top);
             if (lane == 0) s.tops[5][warp] = top;
@@ -326,16 +331,19 @@ __global__ void __launch_bounds__(D * 4, D == 64 ? 2 : 1)
             const float sp = pow2_scale(tp, dp_inv), sm = pow2_scale(tm, dm_inv), sc = second ? sm : sp;
             unsigned char* dst = reinterpret_cast<unsigned char*>(second ? s.dm : s.dp);
 #pragma unroll
-            for (int j = 0; j < 8 / kShare; ++j) {
-                if ((j0 + j / 2) * 16 > r0) continue;  // only the lower blocks are read
+            for (int i = 0; i < kMost; ++i) {  // the upper blocks are not read
+                const int at = member + i * kTeam, br = block_row(at), bc = at - br * (br + 1) / 2;
+                if (at >= 10) continue;
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    uint32_t hi, lo;
-                    split2(t[j][2 * q] * sc, t[j][2 * q + 1] * sc, hi, lo);
-                    const uint32_t at = swz<kC>(r0 + (lane >> 2) + q * 8, j0 * 2 + j) + (lane & 3) * 4;
-                    *reinterpret_cast<uint32_t*>(dst + at) = hi;
-                    *reinterpret_cast<uint32_t*>(dst + kC * kC * 2 + at) = lo;
-                }
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t hi, lo;
+                        split2(t[i][q][2 * h] * sc, t[i][q][2 * h + 1] * sc, hi, lo);
+                        const uint32_t to = swz<kC>(br * 16 + (lane >> 2) + h * 8, bc * 2 + q) + (lane & 3) * 4;
+                        *reinterpret_cast<uint32_t*>(dst + to) = hi;
+                        *reinterpret_cast<uint32_t*>(dst + kC * kC * 2 + to) = lo;
+                    }
             }
         }
         __syncthreads();
