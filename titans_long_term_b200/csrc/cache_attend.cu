@@ -133,6 +133,17 @@ __device__ __forceinline__ void registers_down() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
 }
 
+// The sequence with `place` longer ones, out of at most 32, a lane each.
+__device__ __forceinline__ int by_length(const CacheArgs& c, int place, int lane) {
+    const int end = lane < c.B ? max(c.starts[lane], -1) / 2 + cache_count(c, lane) / 2 : -1;  // halves: no overflow
+    int rank = 0;
+    for (int i = 0; i < c.B; ++i) {
+        const int other = __shfl_sync(0xffffffffu, end, i);
+        rank += other > end || (other == end && i < lane);
+    }
+    return __ffs(__ballot_sync(0xffffffffu, lane < c.B && rank == place)) - 1;
+}
+
 template <int D, bool E4M3, int NT, int STAGES>
 __global__ void __launch_bounds__(Plan<E4M3, NT>::kThreads, 1)
     attend_kernel(AttendArgs a, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
@@ -147,9 +158,10 @@ __global__ void __launch_bounds__(Plan<E4M3, NT>::kThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = c.H / c.Hkv;
     const long rows = c.T * G;  // of one key/value head
-    const int units = c.B * c.Hkv, unit = blockIdx.x % units, b = unit / c.Hkv, hk = unit % c.Hkv;
-    // the last rows see the most keys and start first
-    const long row0 = (long)(gridDim.x / units - 1 - blockIdx.x / units) * (NT * kRows);
+    // The CTAs with the most keys start first: of up to 32 sequences the longest one, and of a sequence the last rows
+    const int hk = blockIdx.x % c.Hkv, per = (int)((rows + NT * kRows - 1) / (NT * kRows)), place = blockIdx.x / c.Hkv / per;
+    const int b = c.B <= 32 ? by_length(c, place, lane) : place;
+    const long row0 = (long)(per - 1 - blockIdx.x / c.Hkv % per) * (NT * kRows);
     const int count = cache_count(c, b);
     const long start = c.starts[b];
     const long t_lo = row0 / G, t_hi = min(min(row0 + NT * kRows, rows) - 1, (long)count * G - 1) / G;

@@ -173,6 +173,30 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
     *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
                                               pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
 }
+// Eight token values as they lie in memory.
+template <typename Tok>
+struct Block8;
+template <>
+struct Block8<__nv_bfloat16> {
+    uint4 u;
+    __device__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
+    __device__ void clear() { u = make_uint4(0, 0, 0, 0); }
+    __device__ void get(float (&x)[8]) const { unpack8(u, x); }
+};
+template <>
+struct Block8<float> {
+    float v[8];
+    __device__ void load(const float* p) { load8(p, v); }
+    __device__ void clear() {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0.f;
+    }
+    __device__ void get(float (&x)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = v[i];
+    }
+};
+
 // Eight values, scaled, into one 16-byte block of the tile's hi piece (and of its lo piece, LO bytes further).
 template <int PIECES>
 __device__ __forceinline__ void put8(uint32_t addr, uint32_t lo_offset, const float (&x)[8], float s) {

@@ -80,7 +80,7 @@ __device__ __forceinline__ float2 get2(const void* tile, int row, int block, int
 }
 
 template <int D, typename Tok>
-__global__ void __launch_bounds__(kThreads, D == 64 && sizeof(Tok) == 2 ? 5 : 3) delta_prepare_kernel(DeltaArgs a, DeltaChunk* out, int chunks, int p_pieces) {
+__global__ void __launch_bounds__(kThreads, sizeof(Tok) == 4 ? 3 : D == 64 ? 5 : 4) delta_prepare_kernel(DeltaArgs a, DeltaChunk* out, int chunks, int p_pieces) {
     using Tiles = Shared<D, Tok>;
     constexpr int NP = Tiles::kPieces, VEC = kC * D / 8 / kThreads;  // blocks of eight values of a thread
     extern __shared__ __align__(1024) unsigned char smem[];
@@ -98,24 +98,31 @@ __global__ void __launch_bounds__(kThreads, D == 64 && sizeof(Tok) == 2 ? 5 : 3)
     const long row0 = delta_key_head(a, unit) * a.T + t0;
     float s[2];
     {
-        float x[2][VEC][8], top[2] = {0.f, 0.f};
+        Block8<Tok> raw[2][VEC];
+        float x[8];
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
             const Tok* p = static_cast<const Tok*>(w ? a.q : a.k) + row0 * D;
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                const int block = i * kThreads + tid, row = block / (D / 8);
-                if (row < n) {
-                    load8(p + (long)block * 8, x[w][i]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x[w][i][j] = 0.f;
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) top[w] = fmaxf(top[w], fabsf(x[w][i][j]));
+                const int block = i * kThreads + tid;
+                if (block / (D / 8) < n)
+                    raw[w][i].load(p + (long)block * 8);
+                else
+                    raw[w][i].clear();
             }
-            top[w] = warp_max(top[w]);
-            if (lane == 0) c.tops[w * 4 + warp] = top[w];
+        }
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            float top = 0.f;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                raw[w][i].get(x);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]));
+            }
+            top = warp_max(top);
+            if (lane == 0) c.tops[w * 4 + warp] = top;
         }
         __syncthreads();
         float inv[2];
@@ -127,7 +134,8 @@ __global__ void __launch_bounds__(kThreads, D == 64 && sizeof(Tok) == 2 ? 5 : 3)
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
                 const int block = i * kThreads + tid, row = block / (D / 8);
-                put8<NP>(base + swz<D>(row, block % (D / 8)), kC * D * 2, x[w][i], s[w]);
+                raw[w][i].get(x);
+                put8<NP>(base + swz<D>(row, block % (D / 8)), kC * D * 2, x, s[w]);
             }
         }
         if (tid == 0) o.k_scale = s[0], o.q_scale = s[1], o.k_inv = inv[0], o.q_inv = inv[1];

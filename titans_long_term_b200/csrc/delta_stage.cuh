@@ -143,30 +143,6 @@ __device__ __forceinline__ void times_tokens(float (&out)[4][4], const float (&w
     }
 }
 
-// Eight token values as they lie in memory.
-template <typename Tok>
-struct Block8;
-template <>
-struct Block8<__nv_bfloat16> {
-    uint4 u;
-    __device__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
-    __device__ void clear() { u = make_uint4(0, 0, 0, 0); }
-    __device__ void get(float (&x)[8]) const { unpack8(u, x); }
-};
-template <>
-struct Block8<float> {
-    float v[8];
-    __device__ void load(const float* p) { load8(p, v); }
-    __device__ void clear() {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0.f;
-    }
-    __device__ void get(float (&x)[8]) const {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = v[i];
-    }
-};
-
 // What thread p of the producers brings of a chunk: K, the CTA's columns of V (or dY) and, WITH_Q, Q and P too. The tokens are
 // fetched into registers while the chunks before are still in work: one round trip to memory a chunk, which nothing waits for.
 template <int D, int RW, typename Tok, int PP, bool WITH_Q>
