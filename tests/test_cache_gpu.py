@@ -1,4 +1,6 @@
 """The paged cache and its attention on the GPU against the definition in 64 bits (cache_ref)."""
+import gc
+
 import pytest
 import torch
 
@@ -212,6 +214,7 @@ def test_other_stream_and_graph():
     o1 = p.cache.attend(q, p.pages, p.table, starts, o=torch.empty_like(q), stream=s)
     torch.cuda.synchronize()
     assert torch.equal(o, o1)
+    gc.collect()  # handles of other memories that are still waiting to be collected would end the capture
     graph = torch.cuda.CUDAGraph()
     z = q.clone()
     with torch.cuda.graph(graph):
@@ -223,6 +226,19 @@ def test_other_stream_and_graph():
     starts.copy_(ints(100, 0))  # the captured call reads where the sequences stand when it runs
     graph.replay()
     assert torch.equal(o2, p.cache.attend(q, p.pages, p.table, starts))
+
+
+def test_a_handle_may_go_while_a_graph_is_captured():
+    p, other = (Pool(1, 2, 2, 64, "bf16", 16, 64, seed=i) for i in range(2))
+    q, starts = p.q(2), ints(60)
+    want = p.cache.attend(q, p.pages, p.table, starts)
+    gc.collect()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        other.cache.close()
+        o = p.cache.attend(q, p.pages, p.table, starts)
+    graph.replay()
+    assert torch.equal(o, want)
 
 
 def test_binding_refuses_tensors():

@@ -89,6 +89,9 @@ def test_binding_refuses():
     with pytest.raises(ValueError):
         DeltaMemory(64, "fp16", 1, 4)
     m = DeltaMemory(64, "bf16", 1, 4)
+    with pytest.raises(TitansError) as e:
+        m._workspace_bytes(1 << 25, 0)
+    assert e.value.status == mem.EUNSUPPORTED and "2^31" in str(e.value)
     x = delta_ref.inputs(1, 4, 4, 8, 64, "bf16")
     with pytest.raises(ValueError, match="CUDA"):
         m.forward(x["k"], x["q"], x["v"], x["g"], x["beta"], {"W": x["W"]})

@@ -1,10 +1,12 @@
 """The gated delta rule on the GPU against the recurrence in 64 bits (delta_ref)."""
+import gc
+
 import pytest
 import torch
 
 import delta_ref
 from delta_ref import assert_close
-from titans_long_term_b200 import DeltaMemory, Memory, PagedCache
+from titans_long_term_b200 import DeltaMemory
 
 pytestmark = pytest.mark.gpu
 
@@ -123,6 +125,7 @@ def test_other_stream_and_outputs():
     assert torch.equal(y0, y1) and torch.equal(W0, W1)
     z = {n: t.clone() for n, t in x.items()}
     W = {"W": z["W"].clone()}
+    gc.collect()  # handles of other memories that are still waiting to be collected would end the capture
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         y2 = m.forward(z["k"], z["q"], z["v"], z["g"], z["beta"], W, lengths=z["lengths"])
@@ -237,6 +240,7 @@ def test_backward_repeats_and_captures():
     s.wait_stream(torch.cuda.current_stream())
     second = grads(m, x, stream=s)
     torch.cuda.synchronize()
+    gc.collect()  # handles of other memories that are still waiting to be collected would end the capture
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         third = m.backward(x["k"], x["q"], x["v"], x["g"], x["beta"], {"W": x["W"]}, x["dy"],

@@ -254,7 +254,12 @@ titans_status_t titans_cache_init(const titans_cache_config* cfg, titans_cache_t
 
 titans_status_t titans_cache_destroy(titans_cache_t c) {
     if (!c) return fail(TITANS_EINVAL, "handle is NULL");
+    // A binding may let go of a handle at any time, also while this thread captures a graph, which a plain cudaFree
+    // would end.
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    const bool swapped = cudaThreadExchangeStreamCaptureMode(&mode) == cudaSuccess;
     cudaFree(c->status);
+    if (swapped) cudaThreadExchangeStreamCaptureMode(&mode);
     delete c;
     return TITANS_OK;
 }

@@ -79,7 +79,8 @@ class DeltaMemory:
             n = lib().titans_delta_workspace_bytes(self._ref, T, call)
             if n == ctypes.c_size_t(-1).value:
                 msg = lib().titans_last_error_string().decode()
-                raise TitansError(lib().titans_delta_step(self._ref, *[None] * 8, None), msg)
+                # the call itself refuses the configuration and T before anything else, with the status for it
+                raise TitansError(lib().titans_delta_forward(self._ref, *[None] * 6, T, *[None] * 4, 0, None), msg)
             self._bytes[(T, call)] = n
         return n
 
