@@ -275,3 +275,11 @@ def test_positions_behind_the_table(T):
     with pytest.raises(TitansError):
         p.cache.sync_status()
     assert (o[0] == 0).all() and (o[1] != 0).any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("T,H,counts", [(6, 1, [3]), (4, 4, [1]), (2, 2, [0])])
+def test_attend_padded_rows_of_a_split_sequence(T, H, counts, dtype):
+    """Keys of one head shared out over several CTAs, whose parts are joined: the rows behind the count are zeros still."""
+    p = Pool(1, H, 1, 64, dtype, 64, 4000, seed=T)
+    check(p, T, ints(4000 - T), counts=ints(*counts))

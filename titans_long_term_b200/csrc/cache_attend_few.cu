@@ -422,16 +422,21 @@ __device__ __forceinline__ void attend_head(const AttendArgs& a, int b, int hk, 
         if (row < seen_rows && !__all_sync(0xffffffffu, fine))
             attend_row<D, E4M3, KEYS>(a, b, hk, static_cast<const __nv_bfloat16*>(a.q) + orow * D, start + t, tiles, first,
                                       last, top, sum, acc);
+        if (row >= seen_rows) {  // a row behind the sequence's count sees nothing
+            top = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < N; ++j) acc[j] = 0.f;
+        }
         if (part) {
             const long prow = place * kM + row;
 #pragma unroll
             for (int j = 0; j < N; ++j) a.part[prow * D + lane * N + j] = acc[j];
             if (lane == 0) a.part_ml[prow] = make_float2(top, sum);
         } else {
-            const float inv = sum == 0.f || row >= seen_rows ? 0.f : 1.f / sum;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
             for (int j = 0; j < N; ++j)
-                static_cast<__nv_bfloat16*>(a.o)[orow * D + lane * N + j] = __float2bfloat16(inv == 0.f ? 0.f : acc[j] * inv);
+                static_cast<__nv_bfloat16*>(a.o)[orow * D + lane * N + j] = __float2bfloat16(acc[j] * inv);
         }
     }
     __syncthreads();  // the next head's outputs come into the same places
