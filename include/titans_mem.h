@@ -379,7 +379,8 @@ titans_status_t titans_delta_backward(const titans_delta_config *cfg, const void
  * The attention branch beside a memory: keys and values of B sequences in pages of `page` tokens,
  * attention of a chunk of new tokens (one or more) over them, in bf16. Its output is what the gated
  * calls above take as `attn`.
- * Token p of sequence b lies in page table[b, p / page], slot p % page. */
+ * Token p of sequence b lies in page table[b, p / page], slot p % page. No output of a call may overlap an input.
+ * Calls with the same handle may run at the same time as long as they share no workspace and no output. */
 typedef enum {
     TITANS_CACHE_BF16 = 0,
     TITANS_CACHE_E4M3 = 1 /* 8-bit floats with one power-of-two scale per token and head: the smallest
@@ -393,11 +394,12 @@ typedef struct {
     int B, H, Hkv;            /* sequences, query heads, key/value heads (Hkv divides H) */
     int page;                 /* tokens of a page: 16, 32, 64 or 128 */
     int num_pages;            /* pages of the pool */
-    int max_pages;            /* entries of a sequence's row of the page table */
+    int max_pages;            /* entries of a sequence's row of the page table; max_pages * page <= 2^31 - 1024 */
 } titans_cache_config;
 
 /* The pool, owned by the caller: k, v [num_pages, Hkv, page, d] bf16 or e4m3 bytes, 16-byte aligned;
- * k_scale, v_scale [num_pages, Hkv, page] fp32 (e4m3 only, else NULL). */
+ * k_scale, v_scale [num_pages, Hkv, page] fp32 (e4m3 only, else NULL): powers of two, as append writes them. A slot
+ * that no append has written may hold anything as long as no query sees it. */
 typedef struct {
     void *k, *v;
     float *k_scale, *v_scale;
@@ -418,7 +420,8 @@ titans_status_t titans_cache_sync_status(titans_cache_t c, void *stream);
  * Writes T new tokens of every sequence at positions starts[b] + t, t < counts[b].
  *   k, v    [B, Hkv, T, d] bf16
  *   table   [B, max_pages] int32; starts [B] int32 >= 0; counts [B] int32 or NULL (all T), clamped to 0..T
- * Nothing else in the pool is touched. Where two tokens of a call share a slot, either may be kept.
+ * Nothing else in the pool is touched. Two tokens of a call must not share a slot (two
+ * sequences on one page, at the same position of it): what it holds then is undefined.
  */
 titans_status_t titans_cache_append(titans_cache_t c, const void *k, const void *v, long T,
                                     const titans_cache_pages *pages, const int *table, const int *starts,
@@ -434,7 +437,7 @@ titans_status_t titans_cache_read(titans_cache_t c, const titans_cache_pages *pa
  * positions). Query t of sequence b stands at p = starts[b] + t and sees the keys j <= p; with
  * window > 0 only those with j > p - window or j < sinks (persistent tokens at the front).
  *   q, o  [B, H, T, d] bf16; head h reads key/value head h / (H / Hkv)
- *   scale  factor of q.k before the softmax, finite
+ *   scale  factor of q.k before the softmax, |scale| <= 2^100
  *   workspace  titans_cache_attend_workspace_bytes(c, T) bytes, 16-byte aligned (NULL where that is 0)
  * A row that sees no key, and the rows t >= counts[b], are zeros. A key that a row does not see does not
  * reach it, infinities and NaN included. Scores, softmax and sums in fp32, the weights rounded to bf16

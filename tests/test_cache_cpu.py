@@ -37,3 +37,11 @@ def test_binding_refuses():
         PagedCache(64, "int8", 1, 1, num_pages=1, max_pages=1)
     with pytest.raises(mem.TitansError):
         PagedCache(64, "bf16", 1, 1)  # no pages
+
+
+def test_a_table_as_long_as_positions_reach():
+    """Positions are 32-bit, also when rounded up to a whole tile of keys."""
+    c = mem.CacheConfig(*{**GOOD, "page": 128, "max_pages": (1 << 24) - 1}.values())
+    h = ctypes.c_void_p(1)
+    assert mem.lib().titans_cache_init(ctypes.byref(c), ctypes.byref(h)) == mem.EUNSUPPORTED
+    assert h.value is None

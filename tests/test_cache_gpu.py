@@ -283,3 +283,17 @@ def test_attend_padded_rows_of_a_split_sequence(T, H, counts, dtype):
     """Keys of one head shared out over several CTAs, whose parts are joined: the rows behind the count are zeros still."""
     p = Pool(1, H, 1, 64, dtype, 64, 4000, seed=T)
     check(p, T, ints(4000 - T), counts=ints(*counts))
+
+
+def test_attend_refuses_what_an_int_or_float_cannot_hold():
+    p = Pool(1, 2, 2, 64, "bf16", 16, 64)
+    q, starts = p.q(3), ints(0)
+    for bad in (dict(window=1 << 31), dict(window=(1 << 32) + 5), dict(sinks=1 << 32)):
+        with pytest.raises(ValueError):
+            p.cache.attend(q, p.pages, p.table, starts, **bad)
+    for scale in (2.0**101, -(2.0**120), float("inf")):
+        with pytest.raises(TitansError) as e:
+            p.cache.attend(q, p.pages, p.table, starts, scale=scale)
+        assert e.value.status == mem.EINVAL
+    most = (1 << 31) - 1
+    check(p, 3, ints(50), window=most, sinks=most)

@@ -105,6 +105,8 @@ class PagedCache:
         `window` > 0 only those with j > p - window or j < sinks; scale defaults to d^-1/2. Rows t >= counts[b]
         are zeros. Returns o [B, H, T, d] bf16, ready to be the `attn` of a gated memory."""
         T, shape = q.shape[-2], (self.B, self.H, q.shape[-2], self.d)
+        if max(abs(window), abs(sinks)) >= 1 << 31:  # beyond any position, and what the call's int holds
+            raise ValueError(f"window and sinks: expected magnitudes below 2^31, got {window} and {sinks}")
         _need(self._index, ("q", q, torch.bfloat16, shape))
         if o is not None:
             _need(self._index, ("o", o, torch.bfloat16, shape))

@@ -170,8 +170,8 @@ titans_status_t check_cfg(const titans_cache_config* c) {
     if (c->d != 64 && c->d != 128) return fail(TITANS_EUNSUPPORTED, "d must be 64 or 128");
     if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128)
         return fail(TITANS_EUNSUPPORTED, "page must be 16, 32, 64 or 128");
-    if ((long)c->max_pages * c->page >= (1L << 31))
-        return fail(TITANS_EUNSUPPORTED, "max_pages * page must be below 2^31");
+    if ((long)c->max_pages * c->page > (1L << 31) - 1024)  // positions, rounded up to a tile or two, are 32-bit
+        return fail(TITANS_EUNSUPPORTED, "max_pages * page must be at most 2^31 - 1024");
     if ((long)c->num_pages * c->Hkv * c->page >= (1L << 31))
         return fail(TITANS_EUNSUPPORTED, "num_pages * Hkv * page must be below 2^31");
     return TITANS_OK;
@@ -316,7 +316,7 @@ titans_status_t titans_cache_attend(titans_cache_t c, const void* q, long T, con
     if (s == TITANS_OK) s = check_ptr(o, "o", 16);
     if (s != TITANS_OK) return s;
     if (window < 0 || sinks < 0) return fail(TITANS_EINVAL, "window and sinks must be >= 0");
-    if (!std::isfinite(scale)) return fail(TITANS_EINVAL, "scale must be finite");
+    if (!(std::fabs(scale) <= 0x1p100f)) return fail(TITANS_EINVAL, "|scale| must be at most 2^100");
     const size_t need = titans_cache_attend_workspace_bytes(c, T);
     if ((s = check_ptr(workspace, "workspace", 16, need == 0)) != TITANS_OK) return s;
     if (workspace_bytes < need) return fail(TITANS_EINVAL, "workspace is too small");
