@@ -14,8 +14,15 @@
 //   O^T += V^T P^T: row m of an output tile may stand for any d, so lane / 4 takes a piece of consecutive d, whose values
 //                   2 i and 2 i + 1 belong to tile i; the values of two keys are paired by a byte permutation.
 // With keys and values as the 16-row side, eight rows of Q (one token of up to eight heads) cost half the registers and
-// instructions of the other way round, and instructions, not bytes, bound that: 12 or 16 warps fit an SM.
-// While one block is multiplied the next one's keys and values are on their way, 64 KiB an SM or more.
+// instructions of the other way round. While one block is multiplied the next one's keys and values are on their way, 8 (bf16)
+// or 4 KiB a warp. What bounds it: the instructions of the conversion and the products (e4m3) or the loads in flight (bf16), and the
+// latency of the dependent loads and the join where there is little to read. One token of 16 heads on 4, d = 128, over 8192 keys:
+//   sequences   bf16              e4m3
+//   1           18.5 us           18.5 us
+//   8           34 us             29 us
+//   32          82 us (6.5 TB/s)  68 us (4.0 TB/s)
+// The tile kernel takes 21, 49 and 99 us (bf16) and 25, 55 and 152 us (e4m3). Up to 16 rows this kernel is as fast or faster, except for 16 rows
+// of many bf16 sequences (32: 112 us against 100).
 // A page holds at least 16 tokens, so 16 keys need one look into the page table, two blocks ahead of their use.
 //
 // An e4m3 cache is multiplied in fp16, to which one instruction converts two values exactly. Q goes to fp16
@@ -32,6 +39,7 @@ namespace titans {
 namespace {
 
 constexpr int kM = 16;
+constexpr int kMostCtas = 148;  // one an SM
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -78,6 +86,8 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 template <int D, bool E4M3, int NQ>
 struct Few {
     static constexpr int kKeys = kBlock, kSub = kKeys / 16;  // keys of a block, in sixteens
+    // Loads in flight against registers: with 8 rows 12 warps (32 sequences: 84 us against 91 with 8; e4m3 71 against 85), with 16
+    // rows 8 (114 us against 154 with 12, which spill; e4m3 110 against 107)
     static constexpr int kWarps = NQ == 2 ? 8 : 12;
     static constexpr int kRows = 8 * NQ;
     static constexpr int kBytes = kWarps * kRows * (D * (int)sizeof(float) + (int)sizeof(float2));
@@ -498,39 +508,76 @@ __global__ void __launch_bounds__(Few<D, E4M3, NQ>::kWarps * 32, 1) attend_few_k
     }
 }
 
-// The rows of the heads whose keys more than one CTA had, and of sequences without any: one warp a row.
+// The rows of the heads whose keys more than one CTA had, and of sequences without any: one warp a row. A sequence that is
+// alone may have all CTAs' parts, so the lanes look up their maxima and sums at once, and the outputs are read eight at a
+// time (one after the other, with their divisions, cost 30 us for one sequence of 8192 keys).
 template <int D, int KEYS>
 __global__ void __launch_bounds__(128) join_kernel(AttendArgs a, int ctas) {
-    constexpr int N = D / 32;
+    constexpr int N = D / 32, kEach = (kMostCtas + 31) / 32, kAhead = 8;
     const CacheArgs& c = a.c;
     const int G = c.H / c.Hkv, rows = (int)c.T * G, lane = threadIdx.x & 31;
-    const long at = (long)blockIdx.x * 4 + (threadIdx.x >> 5), unit = at / rows;
-    if (unit >= (long)c.B * c.Hkv) return;
-    const int row = (int)(at % rows), b = (int)(unit / c.Hkv), hk = (int)(unit % c.Hkv);
+    const unsigned at = blockIdx.x * 4 + (threadIdx.x >> 5), unit = at / (unsigned)rows;  // B * H * T is below 2^31
+    if (unit >= (unsigned)c.B * c.Hkv) return;
+    const int row = (int)(at % (unsigned)rows), b = (int)(unit / c.Hkv), hk = (int)(unit % c.Hkv);
     const int n = tiles_of<KEYS>(keys_of(a, b)).count;
-    float top = -INFINITY, sum = 0.f, acc[N] = {};
+    float sum = 0.f, acc[N] = {};
     if (n > 0) {
         const long total = a.begins[c.B], x0 = a.begins[b] + (long)hk * n;
         const int c0 = owner(x0, ctas, total), c1 = owner(x0 + n - 1, ctas, total);
         if (c0 == c1) return;  // written already
+        const long place0 = 2L * c0 + (x0 > total * c0 / ctas);  // the first part ends its CTA's range, the others begin theirs
+        auto place = [&](int i) { return (i == 0 ? place0 : 2L * (c0 + i)) * kM + row; };
+        float2 ml[kEach];
+        float top = -INFINITY;
         bool nan = false;
-        auto idle = [&](int i) { return total * i / ctas == total * (i + 1) / ctas; };  // fewer blocks than CTAs
-        auto place = [&](int i) { return ((long)i * 2 + (i == c0 && x0 > total * i / ctas)) * kM + row; };
-        for (int i = c0; i <= c1; ++i) {
-            if (idle(i)) continue;
-            const float m = a.part_ml[place(i)].x;
-            top = fmaxf(top, m);
-            nan = nan || m != m;
-        }
-        for (int i = c0; i <= c1; ++i) {
-            if (idle(i)) continue;
-            const float2 ml = a.part_ml[place(i)];
-            if (ml.x == -INFINITY && ml.y == 0.f) continue;
-            const float f = nan ? NAN : ml.x == top ? 1.f : ex2(ml.x - top);
-            sum = fmaf(ml.y, f, sum);
 #pragma unroll
-            for (int j = 0; j < N; ++j) acc[j] = fmaf(a.part[place(i) * D + lane * N + j], f, acc[j]);
+        for (int k = 0; k < kEach; ++k) {
+            const int i = 32 * k + lane, cta = c0 + i;
+            ml[k] = make_float2(-INFINITY, 0.f);
+            if (cta <= c1 && total * cta / ctas != total * (cta + 1) / ctas)  // with fewer blocks than CTAs some are idle
+                ml[k] = a.part_ml[place(i)];
+            top = fmaxf(top, ml[k].x);
+            nan = nan || ml[k].x != ml[k].x;
         }
+#pragma unroll
+        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        nan = __any_sync(0xffffffffu, nan);
+        float f[kEach];
+        uint32_t there[kEach];
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const bool some = !(ml[k].x == -INFINITY && ml[k].y == 0.f);
+            there[k] = __ballot_sync(0xffffffffu, some);
+            f[k] = !some ? 0.f : nan ? NAN : ml[k].x == top ? 1.f : ex2(ml[k].x - top);
+            sum = fmaf(ml[k].y, f[k], sum);
+        }
+#pragma unroll
+        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+#pragma unroll
+        for (int k = 0; k < kEach; ++k)
+#pragma unroll
+            for (int i0 = 0; i0 < 32; i0 += kAhead) {
+                if ((there[k] >> i0 & ((1u << kAhead) - 1)) == 0) continue;
+                float x[kAhead][N];
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    const float* p = a.part + place(32 * k + i0 + i) * D + lane * N;
+                    const bool is = there[k] >> (i0 + i) & 1;
+                    if constexpr (N == 4) {
+                        const float4 u = is ? *reinterpret_cast<const float4*>(p) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        x[i][0] = u.x, x[i][1] = u.y, x[i][2] = u.z, x[i][3] = u.w;
+                    } else {
+                        const float2 u = is ? *reinterpret_cast<const float2*>(p) : make_float2(0.f, 0.f);
+                        x[i][0] = u.x, x[i][1] = u.y;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    const float w = __shfl_sync(0xffffffffu, f[k], i0 + i);
+#pragma unroll
+                    for (int j = 0; j < N; ++j) acc[j] = fmaf(x[i][j], w, acc[j]);
+                }
+            }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const long orow = ((long)b * c.H + hk * G + row % G) * c.T + row / G;
@@ -558,7 +605,7 @@ cudaError_t launch(const AttendArgs& a, int ctas, cudaStream_t st) {
 
 // One CTA an SM, and at least 16 blocks of the longest possible sequences each, two a warp.
 int ctas_for(int B, int Hkv, long longest) {
-    return (int)std::max(1L, std::min(148L, (longest / 16 * B * Hkv + 15) / 16));
+    return (int)std::max(1L, std::min((long)kMostCtas, (longest / 16 * B * Hkv + 15) / 16));
 }
 
 }  // namespace
