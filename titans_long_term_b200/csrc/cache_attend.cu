@@ -17,7 +17,7 @@
 // A masked weight is 0, but 0 times an infinity or NaN that another row of the tile does see is NaN. Rows that come
 // out non-finite are therefore taken again key by key over just what they see (attend_row).
 //
-// With few rows the keys are split over CTAs, each of which leaves its sum, maximum and unnormalised output in the
+// Where there are few tiles of rows the keys are split over CTAs, each of which leaves its sum, maximum and unnormalised output in the
 // workspace for combine_kernel.
 #include <algorithm>
 #include <type_traits>
@@ -30,6 +30,7 @@ namespace {
 
 constexpr int kKeys = 128;  // keys of a tile
 constexpr int kRows = 128;  // rows of a tile
+constexpr long kSms = 148;
 constexpr float kLazy = 8.f;
 
 template <int D, int NT, int STAGES>
@@ -699,32 +700,38 @@ cudaError_t launch(const AttendArgs& a, int splits, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-// Splits of the keys: enough CTAs for two rounds over the SMs, and no less than four tiles of the longest
-// possible sequence each. The lengths themselves are on the device.
-int tile_splits(int B, int H, int Hkv, long T, long longest) {
-    const long rows = T * (H / Hkv), base = ((rows + kRows - 1) / kRows) * B * Hkv;
-    const long most = std::max(1L, longest / kKeys / 4);
-    return (int)std::max(1L, std::min({most, 2 * 148L / base, 64L}));
+// How the rows and keys are shared out: tiles of rows a CTA, and splits of the keys. One CTA fits an SM, and more splits than
+// fill one round of them only add parts to join (128 rows of 16 heads, 8192 keys: 35 us with 148 CTAs at most, 48 us with
+// 296); a split has no less than four tiles of the longest possible sequence, the lengths themselves are on the device.
+// A CTA with two tiles of rows takes 1.45 times as long as one with one (2048 tokens of 16 heads, 8000 keys: 138 us in one
+// round, 191 us in two), so it is the choice where it does not leave too many SMs idle.
+struct Shares {
+    int tiles, splits;
+};
+Shares shares(int B, int H, int Hkv, long T, long longest) {
+    const long rows = T * (H / Hkv), most = std::min(64L, (longest + 4 * kKeys - 1) / (4 * kKeys));
+    auto splits = [&](long ctas) { return std::max(1L, std::min(most, kSms / ctas)); };
+    auto rounds = [&](long ctas) { return (double)((ctas * splits(ctas) + kSms - 1) / kSms) / splits(ctas); };
+    const long one = (rows + kRows - 1) / kRows * B * Hkv, two = (rows + 2 * kRows - 1) / (2 * kRows) * B * Hkv;
+    return 1.45 * rounds(two) < rounds(one) ? Shares{2, (int)splits(two)} : Shares{1, (int)splits(one)};
 }
 
 }  // namespace
 
 size_t attend_workspace_bytes(int B, int H, int Hkv, long T, int d, long longest) {
     if (attend_few_rows(H, Hkv, T)) return attend_few_bytes(B, Hkv, d, longest);
-    const int splits = tile_splits(B, H, Hkv, T, longest);
+    const int splits = shares(B, H, Hkv, T, longest).splits;
     return splits == 1 ? 0 : (size_t)splits * B * H * T * (d * sizeof(float) + sizeof(float2));
 }
 
 cudaError_t launch_cache_attend(const AttendArgs& args, bool e4m3, void* workspace, long longest, cudaStream_t st) {
     if (attend_few_rows(args.c.H, args.c.Hkv, args.c.T)) return launch_attend_few(args, e4m3, workspace, longest, st);
     AttendArgs a = args;
-    const int splits = tile_splits(a.c.B, a.c.H, a.c.Hkv, a.c.T, longest);
+    const auto [tiles, splits] = shares(a.c.B, a.c.H, a.c.Hkv, a.c.T, longest);
     const size_t n = (size_t)splits * a.c.B * a.c.H * a.c.T;
     a.part = static_cast<float*>(workspace);
     a.part_ml = reinterpret_cast<float2*>(a.part + (splits > 1 ? n * a.c.d : 0));
-    // Two tiles of rows a CTA where that still leaves a CTA for most SMs
-    const long rows = a.c.T * (a.c.H / a.c.Hkv);
-    const bool two = rows > kRows && (rows + 2 * kRows - 1) / (2 * kRows) * a.c.B * a.c.Hkv * splits >= 100;
+    const bool two = tiles == 2;
     cudaError_t e;
     if (a.c.d == 64) {
         e = e4m3 ? (two ? launch<64, true, 2>(a, splits, st) : launch<64, true, 1>(a, splits, st))
