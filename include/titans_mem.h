@@ -341,7 +341,7 @@ typedef struct {
  *            (as titans_mem_forward_gated)
  *   workspace  device memory of titans_delta_workspace_bytes(cfg, T, 0) bytes, 16-byte aligned
  *            (NULL where that is 0); nothing in it is kept between calls
- * T >= 1, T * d < 2^31 and B * H * ceil(T / 64) < 2^30. Up to 16 tokens in fp32 arithmetic, one by one; more in
+ * T >= 1, T * d < 2^31 and B * H * ceil(T / 64) < 2^30. Up to 24 tokens in fp32 arithmetic, one by one; more in
  * chunks of 64 tokens on the tensor cores, with operands split into fp16 pieces that together hold 22 bits of a
  * value down to 2^-16 of the largest one of its row or chunk (below that, an absolute error of 2^-39 of the largest);
  * for a bf16 y, 11 bits of the state and the writes. An infinity or NaN among a unit's tokens may reach all

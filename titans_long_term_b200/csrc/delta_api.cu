@@ -79,9 +79,10 @@ titans::DeltaArgs make_args(const titans_delta_config* c, const void* k, const v
     return a;
 }
 
-// Up to this many tokens go one by one, with the state in registers: the chunked path's two launches and its
-// work on 64 tokens cost more there.
-constexpr long kTokens = 16;
+// Up to this many tokens go one by one, with the state in registers: 0.5 us a token, against 16.5 us for the chunked path's two
+// launches and its work on 64 tokens (16 to 128 units, d = 64 and 128: 10.3 us for 16 tokens, 12.4 to 14.5 for 24, 16.5 to
+// 18.5 for 32).
+constexpr long kTokens = 24;
 
 long records(const titans_delta_config* c, long T) { return (long)c->B * c->H * ((T + 63) / 64); }
 struct Backward {  // offsets in the workspace of the backward pass, 1 KiB aligned
