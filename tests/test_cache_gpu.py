@@ -297,3 +297,17 @@ def test_attend_refuses_what_an_int_or_float_cannot_hold():
         assert e.value.status == mem.EINVAL
     most = (1 << 31) - 1
     check(p, 3, ints(50), window=most, sinks=most)
+
+
+def test_attend_many_short_sequences():
+    """More sequences than a warp has lanes, more rows than the kernel for few of them takes, of unlike lengths."""
+    p = Pool(40, 2, 1, 64, "bf16", 16, 100, seed=9)
+    check(p, 20, ints(*[(7 * b) % 81 for b in range(40)]), counts=ints(*[20 - b % 3 for b in range(40)]))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d,window,count", [(64, 0, 256), (128, 900, 131)])
+def test_attend_split_keys_of_two_tiles(d, window, count, dtype):
+    """Two tiles of rows a CTA and keys shared out over several CTAs at once; rows behind the count in some of them."""
+    p = Pool(1, 8, 2, d, dtype, 64, 8000, seed=d)
+    check(p, 256, ints(7744), counts=ints(count), window=window, sinks=30 if window else 0)

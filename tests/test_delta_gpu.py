@@ -249,3 +249,14 @@ def test_backward_repeats_and_captures():
     torch.cuda.synchronize()
     for n in first:
         assert torch.equal(first[n], second[n]) and torch.equal(first[n], third[n]), n
+
+
+@pytest.mark.parametrize("mode", ["bf16", "fp32"])
+@pytest.mark.parametrize("T", [24, 25])
+def test_forward_where_chunks_begin(T, mode):
+    """The longest call that goes token by token, and the shortest one in chunks."""
+    m, x = make(2, 4, 2, T, 128, mode, seed=T)
+    y, W = call(m, x)
+    ry, rW = delta_ref.forward(x)
+    assert_close("y", y, ry, mode)
+    assert_close("W", W, rW, "fp32")

@@ -14,6 +14,8 @@
 //     Y = gamma Q W0^T + P E, its gate and its stores, from the same fragments;
 //   - four producer warps bring the next chunk's K, Q, V, N and P into a second stage of shared memory meanwhile, the tokens
 //     split into fp16 pieces on the way.
+// 128 units of 64 chunks, d = 64: 183 us, 2.9 us a chunk (155 us where the states and eps are left for the backward pass instead of y);
+// 32 units of 256 chunks, d = 128: 732 us, also 2.9 us. One chain warp a tensor core: the issue slots are 36 % busy, HBM 8 %.
 #include "delta_stage.cuh"
 
 namespace titans {
