@@ -50,6 +50,29 @@ __device__ __forceinline__ float max_of(const float* x) {
     return t;
 }
 
+// Four values as floats in memory, and as pieces in a [rows][D] tile: the i-th four of its values lie at quad_at.
+__device__ __forceinline__ void load4(const float* p, float (&x)[4]) {
+    const float4 u = *reinterpret_cast<const float4*>(p);
+    x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
+}
+__device__ __forceinline__ void store4(float* p, const float (&x)[4]) {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&x)[4]) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+}
+template <int D>
+__device__ __forceinline__ uint32_t quad_at(int i) {
+    return swz<D>(i / (D / 4), i % (D / 4) >> 1) + (i & 1) * 8;
+}
+__device__ __forceinline__ void put4(uint32_t addr, uint32_t lo_offset, const float (&x)[4], float s) {
+    uint32_t h[2], l[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) split2(x[2 * i] * s, x[2 * i + 1] * s, h[i], l[i]);
+    asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(addr), "r"(h[0]), "r"(h[1]) : "memory");
+    asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(addr + lo_offset), "r"(l[0]), "r"(l[1]) : "memory");
+}
+
 // a += A B for this warp's 32 tokens of the tile at `left` (NA pieces of [64][LD], 16 steps of k from column k0 on) and its 16 columns of the
 // two-piece tile [64][D] at `right`, rows = k.
 template <int D, int NA>
@@ -106,7 +129,7 @@ __device__ __forceinline__ void times_tokens(float (&t)[2][2][4], uint32_t s, ui
 template <int D, typename Tok>
 __global__ void __launch_bounds__(D * 4, D == 64 ? 2 : 1)
     delta_grads_kernel(DeltaArgs a, const DeltaChunk* recs, int chunks, DeltaGrads g) {
-    constexpr int NP = sizeof(Tok) == 4 ? 2 : 1, kThreads = D * 4, NC = D / 8, VEC = kC * D / 8 / kThreads;  // VEC = 2
+    constexpr int NP = sizeof(Tok) == 4 ? 2 : 1, kThreads = D * 4, NC = D / 8, VEC = kC * D / 8 / kThreads, QUADS = 2 * VEC;  // VEC = 2
     constexpr int VW = D * D / 8 / kThreads;  // blocks of eight values of a state a thread
     using S = Shared<D, NP>;
     constexpr int kWarps = S::kWarps;
@@ -191,48 +214,58 @@ __global__ void __launch_bounds__(D * 4, D == 64 ? 2 : 1)
         if (tid < 144) (&s.to[0][0])[tid] = (&r.to[0][0])[tid];
         float y_inv, e_inv, f_inv, w_inv, a_inv, sw, sa, inner;
         {  // dY, E and F as pieces; dV and dbeta on the way; the states' largest values and <A, W0>
-            float y[VEC][8], e[VEC][8], f[VEC][8], top[5] = {}, dot_wa = 0.f;
+            // Floats are read four a lane, so that a warp's load is one run; tokens in mode bf16 stay raw until they are scaled
+            Block8<Tok> y[VEC];
+            float e[QUADS][4], f[QUADS][4], top[5] = {}, dot_wa = 0.f;
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const int block = i * kThreads + tid, row = block / NC;
-                load8(g.fwd.eps + rec * kC * D + (long)block * 8, e[i]);
-                load8(g.dr + rec * kC * D + (long)block * 8, f[i]);
-                if (row < n) {
-                    load8(static_cast<const Tok*>(g.dy) + tok * D + (long)block * 8, y[i]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) y[i][j] = 0.f;
-                }
+            for (int i = 0; i < QUADS; ++i) {
+                const long at = rec * kC * D + (long)(i * kThreads + tid) * 4;
+                load4(g.fwd.eps + at, e[i]);
+                load4(g.dr + at, f[i]);
             }
 #pragma unroll
-            for (int i = 0; i < VW; ++i) {
-                float x[8], z[8];
-                load8(w0 + (long)(i * kThreads + tid) * 8, x);
-                load8(adj + (long)(i * kThreads + tid) * 8, z);
+            for (int i = 0; i < VEC; ++i) {
+                const int block = i * kThreads + tid;
+                if (block / NC < n)
+                    y[i].load(static_cast<const Tok*>(g.dy) + tok * D + (long)block * 8);
+                else
+                    y[i].clear();
+            }
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+            for (int i = 0; i < 2 * VW; ++i) {
+                float x[4], z[4];
+                load4(w0 + (long)(i * kThreads + tid) * 4, x);
+                load4(adj + (long)(i * kThreads + tid) * 4, z);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
                     top[3] = fmaxf(top[3], fabsf(x[j])), top[4] = fmaxf(top[4], fabsf(z[j]));
                     dot_wa = fmaf(x[j], z[j], dot_wa);
                 }
             }
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                const int block = i * kThreads + tid, row = block / NC;
+                float x[8];
+                y[i].get(x);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) top[0] = fmaxf(top[0], fabsf(x[j]));
+            }
+#pragma unroll
+            for (int i = 0; i < QUADS; ++i) {
+                const int quad = i * kThreads + tid, row = quad / (D / 4);
                 float dot = 0.f;
                 const float beta = r.beta[row];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < 4; ++j) {
                     dot = fmaf(e[i][j], f[i][j], dot);
                     e[i][j] *= beta, f[i][j] *= beta;
-                    top[0] = fmaxf(top[0], fabsf(y[i][j]));
                     top[1] = fmaxf(top[1], fabsf(e[i][j]));
                     top[2] = fmaxf(top[2], fabsf(f[i][j]));
                 }
 #pragma unroll
-                for (int d = NC / 2; d; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
+                for (int d = D / 8; d; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
                 if (row < rows) {
-                    if (block % NC == 0) g.dbeta[tok + row] = row < n ? dot : 0.f;
-                    store8(static_cast<Tok*>(g.dv) + tok * D + (long)block * 8, f[i]);
+                    if (quad % (D / 4) == 0) g.dbeta[tok + row] = row < n ? dot : 0.f;
+                    store4(static_cast<Tok*>(g.dv) + tok * D + (long)quad * 4, f[i]);
                 }
             }
 #pragma unroll
@@ -253,20 +286,24 @@ __global__ void __launch_bounds__(D * 4, D == 64 ? 2 : 1)
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
                 const int block = i * kThreads + tid;
-                const uint32_t at = swz<D>(block / NC, block % NC);
-                put8<NP>(ys + at, kTile, y[i], sy);
-                put8<2>(es + at, kTile, e[i], se);
-                put8<2>(fs + at, kTile, f[i], sf);
+                float x[8];
+                y[i].get(x);
+                put8<NP>(ys + swz<D>(block / NC, block % NC), kTile, x, sy);
+            }
+#pragma unroll
+            for (int i = 0; i < QUADS; ++i) {
+                const uint32_t at = quad_at<D>(i * kThreads + tid);
+                put4(es + at, kTile, e[i], se);
+                put4(fs + at, kTile, f[i], sf);
             }
         }
         // 64 rows of a state into the tile w
         auto stage_state = [&](const float* src, int row0, float sc) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const int block = i * kThreads + tid;
-                float x[8];
-                load8(src + (long)row0 * D + (long)block * 8, x);
-                put8<2>(ws + swz<D>(block / NC, block % NC), kTile, x, sc);
+            for (int i = 0; i < QUADS; ++i) {
+                float x[4];
+                load4(src + (long)row0 * D + (long)(i * kThreads + tid) * 4, x);
+                put4(ws + quad_at<D>(i * kThreads + tid), kTile, x, sc);
             }
         };
         stage_state(w0, 0, sw);
