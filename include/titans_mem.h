@@ -319,11 +319,11 @@ titans_status_t titans_silu_routes(const float *h, float *silu_fma, float *silu_
  * whose queries read it after the write (titans_mem_forward's chunks take it at the chunk-start
  * weights). Per unit, W [d, d] fp32 in the column convention M(x) = W x:
  *   A_t = exp(g_t) W_{t-1},  e_t = beta_t (v_t - A_t k_t),  W_t = A_t + e_t k_t^T,  y_t = W_t q_t.
- * g <= 0 is the log of what is retained (log(1 - alpha) of the other memories; -infinity forgets
- * all), beta the writing strength. H value heads share Hk key/query heads: head h reads key head
- * h / (H / Hk). The calls keep no handle: they read the configuration that they are given, run on
- * the current device, and two calls may run at the same time as long as they share no workspace
- * and no output. No output may overlap an input. */
+ * g <= 0 is the log of what is retained (log(1 - alpha) of the other memories; below -104, where exp
+ * is 0 in fp32, down to -infinity it forgets all that is finite), beta the writing strength. H value
+ * heads share Hk key/query heads: head h reads key head h / (H / Hk). The calls keep no handle: they
+ * read the configuration that they are given, run on the current device, and two calls may run at the
+ * same time as long as they share no workspace and no output. No output may overlap an input. */
 typedef struct {
     int d;              /* width of keys and values: 64 or 128 */
     titans_mode_t mode; /* dtype of k, q, v, attn, y, dy, dk, dq, dv; the state and the gates are fp32 */

@@ -35,7 +35,7 @@ struct DeltaChunk {
     float k_scale, q_scale;               // powers of two that the tiles of K and Q are multiplied by
     float k_inv, q_inv, n_inv, p_inv;     // 1 / the scales
     float ghi[kC], glo[kC];               // G_i as two floats
-    int zeros[kC];                        // decays of 0 (g = -inf) up to token i, which G leaves out
+    int zeros[kC];                        // decays of 0 (g < -104) up to token i, which G leaves out
     float from[kC], to[3][48];            // decays from the end of the block of 16 before token i's to i, and from token
                                           // j to the end of blocks 0, 1 and 2: their product is D_ij between blocks
     float pad[170];

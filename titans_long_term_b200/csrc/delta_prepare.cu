@@ -17,6 +17,7 @@ namespace titans {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr float kForget = -104.f;  // exp of less is 0 in fp32 (half of its least value is exp(-103.97))
 
 template <int D, typename Tok>
 struct Shared {
@@ -145,8 +146,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(Tok) == 4 ? 3 : D == 64 ? 5 :
     }
 
     // The decays, two tokens a lane. G is summed in 64 bits and kept as two floats: D needs the difference of
-    // two sums to fp32's precision of exp(G_i - G_j), however far both are from 0. A decay of 0 (g = -inf) is counted
-    // apart: D_ij = 0 where one lies between, and the others' sums stay finite.
+    // two sums to fp32's precision of exp(G_i - G_j), however far both are from 0. A decay of 0 is counted
+    // apart: D_ij = 0 where one lies between. The others' sums stay above -64 * 104, where neither the sum nor its two
+    // floats lose anything of a token's g, however low the marker that a decay of 0 was given as.
     if (warp == 0) {
         double g[2];
         int zero[2];
@@ -156,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(Tok) == 4 ? 3 : D == 64 ? 5 :
             const int t = 2 * lane + i;
             const float x = t < n ? a.g[unit * a.T + t0 + t] : 0.f;
             beta[i] = t < n ? a.beta[unit * a.T + t0 + t] : 0.f;
-            zero[i] = x == -INFINITY;
+            zero[i] = x < kForget;
             g[i] = zero[i] ? 0.0 : (double)x;
         }
         const double sum = warp_prefix(g[0] + g[1], lane), last = __shfl_sync(0xffffffffu, sum, 31);
