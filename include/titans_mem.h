@@ -441,7 +441,8 @@ titans_status_t titans_cache_read(titans_cache_t c, const titans_cache_pages *pa
  *   workspace  titans_cache_attend_workspace_bytes(c, T) bytes, 16-byte aligned (NULL where that is 0)
  * A row that sees no key, and the rows t >= counts[b], are zeros. A key that a row does not see does not
  * reach it, infinities and NaN included. Scores, softmax and sums in fp32, the weights rounded to bf16
- * for their product with v.
+ * for their product with v; over an e4m3 cache, where the rows of a key/value head (T * H / Hkv) are 16 or
+ * fewer, to 11 bits with an absolute error of at most 2^-32 of the largest product of weight and scale.
  */
 titans_status_t titans_cache_attend(titans_cache_t c, const void *q, long T, const titans_cache_pages *pages,
                                     const int *table, const int *starts, const int *counts, int window,

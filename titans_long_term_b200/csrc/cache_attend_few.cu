@@ -27,8 +27,13 @@
 //
 // An e4m3 cache is multiplied in fp16, to which one instruction converts two values exactly. Q goes to fp16
 // times a power of two of its row (largest element at 2^14..2^15: exact down to 2^-28 of it). Weights go to
-// fp16 as 2^(z + log2 s - M), s the scale of the key's values and M the running maximum of z + log2 s, so that the largest
-// contribution is near 1 whatever the scales are; their sum takes them back by 1 / s, in fp32.
+// fp16 as 2^(7 + z + log2 s - M), s the scale of the key's values and M the running maximum of z + log2 s over the keys whose values
+// are not all zeros. Such a key's largest value is at least 2^7.8 of its scale, so what the fp16 weights lose (half a step, 2^-11
+// of each, and at most 2^-25 where the largest one is 2^7 or more) is small beside the output whatever the scales are. A key without any value
+// has a scale of 1 all the same and would push the others' weights out of fp16's range; it is left out of M and its weight is
+// held below 2^15, as its product is 0 anyway. The sum of the weights knows nothing of the values: each lane keeps it in fp32
+// beside a maximum of its own, of z alone, that the scores may pass by 32. The second exponential of a score costs nothing that
+// shows (32 sequences, d = 128: 77.9 us in place of 78.6 with the sum taken back by 1 / s, which lost what s put out of range).
 #include <algorithm>
 #include <type_traits>
 
@@ -64,6 +69,8 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 constexpr int kBlock = 16;  // keys of a block
+constexpr float kNothing = -3.4028234664e38f;  // below every score
+constexpr float kTopBits = 7.f, kMostWeight = 32768.f;  // e4m3: the weight of the maximum, 2^7, times the 2^8 it may lag behind
 
 // The keys of sequence b that some of its rows see.
 __device__ __forceinline__ Seen keys_of(const AttendArgs& a, int b) {
@@ -151,13 +158,15 @@ __device__ __forceinline__ void attend_head(const AttendArgs& a, int b, int hk, 
         }
     }
     // Rows 8 n + 2 q4 + {0, 1}, whose scores this lane has (keys r and r + 8)
-    float scale[NQ][2], m[NQ][2], l[NQ][2] = {};
+    // m: the running maximum that the weights refer to, the same in all lanes of a row; sum_m (e4m3): what this lane's sum l
+    // refers to, in place of m
+    float scale[NQ][2], m[NQ][2], sum_m[NQ][2], l[NQ][2] = {};
 #pragma unroll
     for (int n = 0; n < NQ; ++n)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             scale[n][h] = a.scale * 1.44269504f * __shfl_sync(0xffffffffu, q_inv[n], (2 * q4 + h) * 4);
-            m[n][h] = -INFINITY;
+            m[n][h] = -INFINITY, sum_m[n][h] = kNothing;
         }
 
     // The page of 16 keys from key0 on; -2 where no row sees any of them. Only the load, so that nothing waits for it
@@ -286,53 +295,99 @@ __device__ __forceinline__ void attend_head(const AttendArgs& a, int b, int hk, 
                     }
                 }
             }
-        // Scores in log2 units (e4m3: plus that of the value's scale); -infinity where the row does not see the key
+        // Scores in log2 units; -infinity where the row does not see the key
         bool whole = key0 >= every_begin && key0 + KEYS <= every.end;
 #pragma unroll
         for (int s = 0; s < SUB; ++s) whole = whole && at[s] >= 0;
-        float inv[SUB][2], top[NQ][2];
+        float v_log[SUB][2], top[NQ][2];  // e4m3: log2 of the values' scales
 #pragma unroll
         for (int n = 0; n < NQ; ++n) top[n][0] = top[n][1] = -INFINITY;
 #pragma unroll
         for (int s = 0; s < SUB; ++s)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {  // keys r, r + 8
-                float k_scale = 1.f, v_log = 0.f;
+                float k_scale = 1.f;
+                v_log[s][e] = 0.f;
                 if constexpr (E4M3) {
-                    k_scale = ks[s][e], v_log = lg2(vs[s][e]);
-                    inv[s][e] = vs[s][e] > 0.f ? __fdividef(1.f, vs[s][e]) : 0.f;
+                    k_scale = ks[s][e];
+                    const float x = lg2(vs[s][e]);
+                    v_log[s][e] = x < 128.f ? x : 0.f;  // a slot that no row sees may hold anything, a NaN too
                 }
 #pragma unroll
                 for (int n = 0; n < NQ; ++n)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         float& x = sc[s][n][2 * e + h];
-                        x = fmaf(x, k_scale * scale[n][h], v_log);
+                        x *= k_scale * scale[n][h];
                         if (!whole) {
                             const Seen v = seen_by(a, start + (8 * n + 2 * q4 + h) / G);
                             if (at[s] < 0 || !v(key0 + 16 * s + 8 * e + r)) x = -INFINITY;
                         }
-                        top[n][h] = fmaxf(top[n][h], x);
+                        top[n][h] = fmaxf(top[n][h], x + v_log[s][e]);
                     }
             }
         load_k(at_next);
         bool grown = false;
+        auto most_of = [&](int n, int h) {  // this lane's largest score of a row
+            float x = sc[0][n][h];
+#pragma unroll
+            for (int s = 0; s < SUB; ++s) x = fmaxf(x, fmaxf(sc[s][n][h], sc[s][n][2 + h]));
+            return x;
+        };
+        auto over_lanes = [&](float x) {  // the largest of a row's eight lanes
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+            return x;
+        };
 #pragma unroll
         for (int n = 0; n < NQ; ++n)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1) top[n][h] = fmaxf(top[n][h], __shfl_xor_sync(0xffffffffu, top[n][h], d));
+                top[n][h] = over_lanes(top[n][h]);
                 grown = grown || top[n][h] - m[n][h] > 8.f || (m[n][h] == -INFINITY && top[n][h] > m[n][h]);
+                if constexpr (E4M3) grown = grown || most_of(n, h) - sum_m[n][h] > 32.f;
             }
         if (__any_sync(0xffffffffu, grown)) {
+            if constexpr (E4M3) {  // once more, without the keys that have no value
+                bool some[SUB][2];
+#pragma unroll
+                for (int s = 0; s < SUB; ++s) {
+                    uint32_t there[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t bits = 0;
+#pragma unroll
+                        for (int g = 0; g < VG; ++g)
+                            bits |= vb[s][e][g].x | vb[s][e][g].y | (VB == 16 ? vb[s][e][g].z | vb[s][e][g].w : 0u);
+                        there[e] = __ballot_sync(0xffffffffu, (bits & 0x7f7f7f7fu) != 0);
+                    }
+                    // key r lies with the lanes q4 = r / 2, as the first or second of their four
+                    const uint32_t lanes = 0x11111111u << (r >> 1);
+                    some[s][0] = (there[r & 1 ? 1 : 0] & lanes) != 0, some[s][1] = (there[r & 1 ? 3 : 2] & lanes) != 0;
+                }
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float x = -INFINITY;
+#pragma unroll
+                        for (int s = 0; s < SUB; ++s)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                if (some[s][e]) x = fmaxf(x, sc[s][n][2 * e + h] + v_log[s][e]);
+                        top[n][h] = over_lanes(x);
+                        const float next = fmaxf(sum_m[n][h], most_of(n, h));
+                        l[n][h] *= ex2(sum_m[n][h] - next);
+                        sum_m[n][h] = next;
+                    }
+            }
 #pragma unroll
             for (int n = 0; n < NQ; ++n)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const float next = fmaxf(m[n][h], top[n][h]), keep = m[n][h] == next ? 1.f : ex2(m[n][h] - next);
                     m[n][h] = next;
-                    l[n][h] *= keep;
+                    if constexpr (!E4M3) l[n][h] *= keep;
 #pragma unroll
                     for (int g = 0; g < VG; ++g)
 #pragma unroll
@@ -349,8 +404,14 @@ __device__ __forceinline__ void attend_head(const AttendArgs& a, int b, int hk, 
                     float x[2];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        x[h] = ex2(sc[s][n][2 * e + h] - (m[n][h] == -INFINITY ? 0.f : m[n][h]));
-                        l[n][h] = E4M3 ? fmaf(x[h], inv[s][e], l[n][h]) : l[n][h] + x[h];
+                        const float shift = m[n][h] == -INFINITY ? 0.f : m[n][h];
+                        if constexpr (E4M3) {
+                            x[h] = fminf(ex2(sc[s][n][2 * e + h] + (v_log[s][e] - shift + kTopBits)), kMostWeight);
+                            l[n][h] += ex2(sc[s][n][2 * e + h] - sum_m[n][h]);
+                        } else {
+                            x[h] = ex2(sc[s][n][2 * e + h] - shift);
+                            l[n][h] += x[h];
+                        }
                     }
                     if constexpr (E4M3) {
                         const __half2 v = __floats2half2_rn(x[0], x[1]);
@@ -399,8 +460,18 @@ __device__ __forceinline__ void attend_head(const AttendArgs& a, int b, int hk, 
     for (int n = 0; n < NQ; ++n)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+            float back = 1.f;  // from the weights' maximum to the sum's
+            if constexpr (E4M3) {
+                float most = sum_m[n][h];
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+                l[n][h] *= ex2(sum_m[n][h] - most);
+                back = ex2(m[n][h] - kTopBits - most);  // 0 where no key had a value
+                m[n][h] = most;
+            }
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) l[n][h] += __shfl_xor_sync(0xffffffffu, l[n][h], d);
+            if (E4M3 && l[n][h] == 0.f) m[n][h] = -INFINITY, back = 0.f;  // no key at all
             const int row = warp * F::kRows + 8 * n + 2 * q4 + h;
             if (r == 0) ml[row] = make_float2(m[n][h], l[n][h]);
 #pragma unroll
@@ -408,7 +479,7 @@ __device__ __forceinline__ void attend_head(const AttendArgs& a, int b, int hk, 
 #pragma unroll
                 for (int e = 0; e < VE / 2; ++e)
                     *reinterpret_cast<float2*>(out + row * D + (g * 8 + r) * VE + 2 * e) =
-                        make_float2(o[g][e][n][h], o[g][e][n][2 + h]);
+                        make_float2(o[g][e][n][h] * back, o[g][e][n][2 + h] * back);
         }
     __syncthreads();
     const bool part = first > 0 || last < tiles.count;
