@@ -413,7 +413,8 @@ typedef struct titans_cache *titans_cache_t;
  * zeros by read and invisible to attend, and recorded in the status word. */
 titans_status_t titans_cache_init(const titans_cache_config *cfg, titans_cache_t *out);
 titans_status_t titans_cache_destroy(titans_cache_t c);
-/* As titans_mem_sync_status. */
+/* As titans_mem_sync_status, by work on `stream` alone: it waits for no other stream, and what calls on other
+ * streams record meanwhile is kept for the next one. */
 titans_status_t titans_cache_sync_status(titans_cache_t c, void *stream);
 
 /*

@@ -120,6 +120,8 @@ __global__ void __launch_bounds__(kThreads) read_kernel(CacheArgs a, uint4* k, u
     v[row * LANES + lane] = z;
 }
 
+__global__ void clear_status_kernel(unsigned* status, unsigned bits) { atomicAnd(status, ~bits); }
+
 unsigned blocks(const CacheArgs& a) {
     const long per = kThreads / (a.d / 8);
     return (unsigned)(((long)a.B * a.Hkv * a.T + per - 1) / per);
@@ -138,6 +140,12 @@ cudaError_t launch_cache_read(const CacheArgs& a, bool e4m3, void* k, void* v, c
     auto* kernel = a.d == 64 ? (e4m3 ? read_kernel<64, true> : read_kernel<64, false>)
                              : (e4m3 ? read_kernel<128, true> : read_kernel<128, false>);
     kernel<<<blocks(a), kThreads, 0, st>>>(a, static_cast<uint4*>(k), static_cast<uint4*>(v));
+    return cudaGetLastError();
+}
+
+// Takes `bits` out of the status word, in the stream's order; bits that another stream sets meanwhile stay.
+cudaError_t launch_clear_status(unsigned* status, unsigned bits, cudaStream_t st) {
+    clear_status_kernel<<<1, 1, 0, st>>>(status, bits);
     return cudaGetLastError();
 }
 
@@ -243,6 +251,8 @@ titans_status_t titans_cache_init(const titans_cache_config* cfg, titans_cache_t
     if (e == cudaSuccess) e = cudaMalloc(&c->status, sizeof(unsigned));
     if (e == cudaSuccess) {
         e = cudaMemset(c->status, 0, sizeof(unsigned));
+        // a first call may come on a stream that does not wait for the default one
+        if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
         if (e != cudaSuccess) cudaFree(c->status);
     }
     if (e != cudaSuccess) {
@@ -267,12 +277,18 @@ titans_status_t titans_cache_destroy(titans_cache_t c) {
 
 titans_status_t titans_cache_sync_status(titans_cache_t c, void* stream) {
     if (!c) return fail(TITANS_EINVAL, "handle is NULL");
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && dev != c->device) e = cudaSetDevice(c->device);
+    if (e != cudaSuccess) return cuda_fail(e, "choosing the handle's device");
+    // All in the caller's stream: the default stream's order would not hold for calls on other streams.
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = cudaStreamSynchronize(st);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize");
     unsigned h = 0;
-    e = cudaMemcpy(&h, c->status, sizeof(unsigned), cudaMemcpyDeviceToHost);
-    if (e == cudaSuccess) e = cudaMemset(c->status, 0, sizeof(unsigned));
+    e = cudaMemcpyAsync(&h, c->status, sizeof(unsigned), cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    if (e == cudaSuccess && h) e = titans::launch_clear_status(c->status, h, st);
+    if (e == cudaSuccess && h) e = cudaStreamSynchronize(st);
+    if (dev != c->device) cudaSetDevice(dev);
     if (e != cudaSuccess) return cuda_fail(e, "reading the status word");
     if (h) return fail(TITANS_EDEVICE, "device status " + std::to_string(h) +
                                            " (2: a wait timed out, 16: a token's page is missing)");
