@@ -385,7 +385,8 @@ typedef enum {
     TITANS_CACHE_BF16 = 0,
     TITANS_CACHE_E4M3 = 1 /* 8-bit floats with one power-of-two scale per token and head: the smallest
                            * 2^e with max |x| <= 448 * 2^e over the finite x (e >= -117; 1 where all are 0).
-                           * Infinities become +-448 * 2^e, NaN stays NaN. */
+                           * Infinities become +-448 * 2^e, NaN stays NaN; with e = 120 magnitudes above
+                           * 240 * 2^120 become that, the largest that bf16 holds too. */
 } titans_cache_type_t;
 
 typedef struct {

@@ -43,11 +43,17 @@ __device__ __forceinline__ uint2 quantise(uint4 u, float& scale) {
     e = top == 0.f ? 0 : max(e, -117);  // -117: the smallest value, 2^-9 of the scale, is a normal bf16 still
     scale = __int_as_float((e + 127) << 23);
     const float inv = __int_as_float((127 - e) << 23);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] *= inv;
+    if (e == 120) {  // 256 * 2^120 would be read back as an infinity; NaN stays NaN
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = fabsf(x[i]) > 240.f ? copysignf(240.f, x[i]) : x[i];
+    }
     uint2 r;
     uint16_t h[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        h[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i] * inv, x[2 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+        h[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i], x[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
     r.x = h[0] | (uint32_t)h[1] << 16;
     r.y = h[2] | (uint32_t)h[3] << 16;
     return r;
