@@ -8,6 +8,8 @@
 
 namespace titans {
 
+constexpr long kSms = 148;  // of a B200
+
 cudaError_t launch_cache_append(const CacheArgs& a, bool e4m3, const void* k, const void* v, cudaStream_t st);
 cudaError_t launch_cache_read(const CacheArgs& a, bool e4m3, void* k, void* v, cudaStream_t st);
 

@@ -34,7 +34,6 @@ namespace {
 
 constexpr int kKeys = 128;  // keys of a tile
 constexpr int kRows = 128;  // rows of a tile
-constexpr long kSms = 148;
 constexpr float kLazy = 8.f;
 
 template <int D, int NT, int STAGES>
@@ -66,12 +65,6 @@ __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n .reg .pred P;\n elect.sync _|P, 0xffffffff;\n selp.u32 %0, 1, 0, P;\n}" : "=r"(p));
     return p != 0;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 __device__ __forceinline__ void bar_sync_producers(int threads) {
@@ -130,14 +123,6 @@ struct Plan {
     static constexpr int kIssueRegs = E4M3 ? 56 : 64, kProducerRegs = 72;
     static constexpr int kShares = kSoftmax * kSoftmaxRegs + 128 * kIssueRegs + (E4M3 ? 256 * kProducerRegs : 0);
 };
-template <int REGS>
-__device__ __forceinline__ void registers_up() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
-}
-template <int REGS>
-__device__ __forceinline__ void registers_down() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
-}
 
 // The sequence with `place` longer ones, out of at most 32, a lane each.
 __device__ __forceinline__ int by_length(const CacheArgs& c, int place, int lane) {

@@ -44,7 +44,7 @@ namespace titans {
 namespace {
 
 constexpr int kM = 16;
-constexpr int kMostCtas = 148;  // one an SM
+constexpr int kMostCtas = kSms;  // one an SM
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -57,18 +57,13 @@ __device__ __forceinline__ float lg2(float x) {
     asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-constexpr int kBlock = 16;  // keys of a block
+constexpr int kBlock = 16;  // keys of a block: the 16 rows of an MMA's A operand, and no page is shorter
 constexpr float kNothing = -3.4028234664e38f;  // below every score
 constexpr float kTopBits = 7.f, kMostWeight = 32768.f;  // e4m3: the weight of the maximum, 2^7, times the 2^8 it may lag behind
 
@@ -82,17 +77,9 @@ __device__ __forceinline__ Seen keys_of(const AttendArgs& a, int b) {
 // The CTA of n whose share of `total` holds block x.
 __device__ __forceinline__ int owner(long x, long n, long total) { return (int)(((x + 1) * n - 1) / total); }
 
-// The 8 x 8 matrix of 16-bit values whose row lane / 4 the lanes hold in pairs, transposed.
-__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
-    uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-    return y;
-}
-
 // NQ: tiles of eight rows.
 template <int D, bool E4M3, int NQ>
 struct Few {
-    static constexpr int kKeys = kBlock, kSub = kKeys / 16;  // keys of a block, in sixteens
     // Loads in flight against registers: with 8 rows 12 warps (32 sequences: 84 us against 91 with 8; e4m3 71 against 85), with 16
     // rows 8 (114 us against 154 with 12, which spill; e4m3 110 against 107)
     static constexpr int kWarps = NQ == 2 ? 8 : 12;
@@ -110,7 +97,7 @@ template <int D, bool E4M3, int NQ>
 __device__ __forceinline__ void attend_head(const AttendArgs& a, int b, int hk, Tiles tiles, int first, int last, long place,
                                             float* smem) {
     using F = Few<D, E4M3, NQ>;
-    constexpr int SUB = F::kSub, KEYS = F::kKeys, KP = F::kKP, KW = F::kKW, VE = F::kVE, VG = F::kVG, W = F::kWarps;
+    constexpr int KEYS = kBlock, KP = F::kKP, KW = F::kKW, VE = F::kVE, VG = F::kVG, W = F::kWarps;
     constexpr int VB = VE * (E4M3 ? 1 : 2);  // bytes: 16, or 8 (e4m3, d = 64)
     const CacheArgs& c = a.c;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, q4 = lane & 3;
@@ -184,155 +171,127 @@ __device__ __forceinline__ void attend_head(const AttendArgs& a, int b, int hk, 
         }
         return ((page * c.Hkv + hk) << c.page_shift) + (key0 & ((1 << c.page_shift) - 1));  // rows are fewer than 2^31
     };
-    uint4 kb[SUB][2][KP];
-    uint4 vb[SUB][4][VG];
-    float ks[SUB][2], vs[SUB][2];  // e4m3: scales of the keys r and r + 8
-    auto load_k = [&](const int(&at)[SUB]) {
+    uint4 kb[2][KP];
+    uint4 vb[4][VG];
+    float ks[2], vs[2];  // e4m3: scales of the keys r and r + 8
+    auto load_k = [&](int at) {
+        if (at < 0) {
 #pragma unroll
-        for (int s = 0; s < SUB; ++s) {
-            if (at[s] < 0) {
+            for (int h = 0; h < 2; ++h) {
+                ks[h] = 0.f;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    ks[s][h] = 0.f;
-#pragma unroll
-                    for (int i = 0; i < KP; ++i) kb[s][h][i] = make_uint4(0, 0, 0, 0);
-                }
-                continue;
+                for (int i = 0; i < KP; ++i) kb[h][i] = make_uint4(0, 0, 0, 0);
             }
-            const uint4* src = static_cast<const uint4*>(c.pk) + (long)(at[s] + r) * (4 * KP) + q4;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int i = 0; i < KP; ++i) kb[s][h][i] = src[32 * KP * h + 4 * i];
-            if constexpr (E4M3) ks[s][0] = c.k_scale[at[s] + r], ks[s][1] = c.k_scale[at[s] + r + 8];
+            return;
         }
+        const uint4* src = static_cast<const uint4*>(c.pk) + (long)(at + r) * (4 * KP) + q4;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < KP; ++i) kb[h][i] = src[32 * KP * h + 4 * i];
+        if constexpr (E4M3) ks[0] = c.k_scale[at + r], ks[1] = c.k_scale[at + r + 8];
     };
     // Values that no row sees are zeros: their weights are 0, and 0 times an infinity or NaN would not be.
-    auto load_v = [&](const int(&at)[SUB], int key0) {
+    auto load_v = [&](int at, int key0) {
+        auto load = [&](auto all) {
+            const char* src = static_cast<const char*>(c.pv) + (long)(at + 2 * q4) * (D * (E4M3 ? 1 : 2)) + r * VB;
 #pragma unroll
-        for (int s = 0; s < SUB; ++s, key0 += 16) {
-            auto load = [&](auto all) {
-                const char* src = static_cast<const char*>(c.pv) + (long)(at[s] + 2 * q4) * (D * (E4M3 ? 1 : 2)) + r * VB;
+            for (int e = 0; e < 4; ++e) {
+                const int k = (e & 1) + (e >> 1) * 8;
+                const bool there = all.value || any(key0 + 2 * q4 + k);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int k = (e & 1) + (e >> 1) * 8;
-                    const bool there = all.value || any(key0 + 2 * q4 + k);
-#pragma unroll
-                    for (int g = 0; g < VG; ++g) {
-                        const char* p = src + k * (D * (E4M3 ? 1 : 2)) + g * 8 * VB;
-                        uint4& v = vb[s][e][g];
-                        if constexpr (!all.value) v = make_uint4(0, 0, 0, 0);
-                        if constexpr (VB == 16) {
-                            if (there) v = *reinterpret_cast<const uint4*>(p);
-                        } else {
-                            uint2 u = make_uint2(0, 0);
-                            if (there) u = *reinterpret_cast<const uint2*>(p);
-                            v.x = u.x, v.y = u.y;
-                        }
+                for (int g = 0; g < VG; ++g) {
+                    const char* p = src + k * (D * (E4M3 ? 1 : 2)) + g * 8 * VB;
+                    uint4& v = vb[e][g];
+                    if constexpr (!all.value) v = make_uint4(0, 0, 0, 0);
+                    if constexpr (VB == 16) {
+                        if (there) v = *reinterpret_cast<const uint4*>(p);
+                    } else {
+                        uint2 u = make_uint2(0, 0);
+                        if (there) u = *reinterpret_cast<const uint2*>(p);
+                        v.x = u.x, v.y = u.y;
                     }
                 }
-            };
-            if (at[s] < 0) {
-                vs[s][0] = vs[s][1] = 0.f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-#pragma unroll
-                    for (int g = 0; g < VG; ++g) vb[s][e][g] = make_uint4(0, 0, 0, 0);
-                continue;
             }
-            if (key0 + 16 <= any.end && (key0 >= any.begin || key0 + 16 <= any.sink_end))
-                load(std::true_type{});
-            else
-                load(std::false_type{});
-            if constexpr (E4M3) vs[s][0] = c.v_scale[at[s] + r], vs[s][1] = c.v_scale[at[s] + r + 8];
+        };
+        if (at < 0) {
+            vs[0] = vs[1] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int g = 0; g < VG; ++g) vb[e][g] = make_uint4(0, 0, 0, 0);
+            return;
         }
+        if (key0 + 16 <= any.end && (key0 >= any.begin || key0 + 16 <= any.sink_end))
+            load(std::true_type{});
+        else
+            load(std::false_type{});
+        if constexpr (E4M3) vs[0] = c.v_scale[at + r], vs[1] = c.v_scale[at + r + 8];
     };
 
     float o[VG][VE / 2][NQ][4] = {};
-    int at[SUB], at_next[SUB];
-    int page[SUB];  // of the block after the next one
-    auto pages_of = [&](int i) {
-#pragma unroll
-        for (int s = 0; s < SUB; ++s) page[s] = i < last ? page_of(tiles[i] * KEYS + 16 * s) : -2;
-    };
-    auto rows_of = [&](int i, int(&x)[SUB]) {
-#pragma unroll
-        for (int s = 0; s < SUB; ++s) x[s] = row_of(page[s], tiles[i] * KEYS + 16 * s);
-    };
-    int i = first + warp;
-    pages_of(i);
-    rows_of(i, at);
-    pages_of(i + W);
+    auto page_at = [&](int i) { return i < last ? page_of(tiles[i] * KEYS) : -2; };
+    int i = first + warp, at = row_of(page_at(i), tiles[i] * KEYS), page = page_at(i + W);  // page: of the block after the next one
     load_k(at);
     load_v(at, tiles[i] * KEYS);
     for (; i < last; i += W) {
-        const int key0 = tiles[i] * KEYS;
-        rows_of(i + W, at_next);
-        pages_of(i + 2 * W);
-        float sc[SUB][NQ][4] = {};
+        const int key0 = tiles[i] * KEYS, at_next = row_of(page, tiles[i + W] * KEYS);
+        page = page_at(i + 2 * W);
+        float sc[NQ][4] = {};
 #pragma unroll
-        for (int s = 0; s < SUB; ++s)
+        for (int j = 0; j < KP; ++j) {
+            const uint32_t x[4] = {kb[0][j].x, kb[0][j].y, kb[0][j].z, kb[0][j].w};
+            const uint32_t y[4] = {kb[1][j].x, kb[1][j].y, kb[1][j].z, kb[1][j].w};
 #pragma unroll
-            for (int j = 0; j < KP; ++j) {
-                const uint32_t x[4] = {kb[s][0][j].x, kb[s][0][j].y, kb[s][0][j].z, kb[s][0][j].w};
-                const uint32_t y[4] = {kb[s][1][j].x, kb[s][1][j].y, kb[s][1][j].z, kb[s][1][j].w};
+            for (int t = 0; t < KW / 2; ++t) {
+                uint32_t f[4];
+                if constexpr (E4M3) {
+                    f[0] = e4m3_to_half2<false>(x[t]), f[1] = e4m3_to_half2<false>(y[t]);
+                    f[2] = e4m3_to_half2<true>(x[t]), f[3] = e4m3_to_half2<true>(y[t]);
+                } else {
+                    f[0] = x[2 * t], f[1] = y[2 * t], f[2] = x[2 * t + 1], f[3] = y[2 * t + 1];
+                }
 #pragma unroll
-                for (int t = 0; t < KW / 2; ++t) {
-                    uint32_t f[4];
-                    if constexpr (E4M3) {
-                        f[0] = e4m3_to_half2<false>(x[t]), f[1] = e4m3_to_half2<false>(y[t]);
-                        f[2] = e4m3_to_half2<true>(x[t]), f[3] = e4m3_to_half2<true>(y[t]);
-                    } else {
-                        f[0] = x[2 * t], f[1] = y[2 * t], f[2] = x[2 * t + 1], f[3] = y[2 * t + 1];
-                    }
-#pragma unroll
-                    for (int n = 0; n < NQ; ++n) {
-                        const uint32_t(&u)[2] = q[n][j * KW / 2 + t];
-                        if constexpr (E4M3)
-                            mma_f16(sc[s][n], f, u[0], u[1]);
-                        else
-                            mma_bf16(sc[s][n], f, u[0], u[1]);
-                    }
+                for (int n = 0; n < NQ; ++n) {
+                    const uint32_t(&u)[2] = q[n][j * KW / 2 + t];
+                    if constexpr (E4M3)
+                        mma_f16(sc[n], f, u[0], u[1]);
+                    else
+                        mma_bf16(sc[n], f, u[0], u[1]);
                 }
             }
+        }
         // Scores in log2 units; -infinity where the row does not see the key
-        bool whole = key0 >= every_begin && key0 + KEYS <= every.end;
-#pragma unroll
-        for (int s = 0; s < SUB; ++s) whole = whole && at[s] >= 0;
-        float v_log[SUB][2], top[NQ][2];  // e4m3: log2 of the values' scales
+        const bool whole = key0 >= every_begin && key0 + KEYS <= every.end && at >= 0;
+        float v_log[2], top[NQ][2];  // e4m3: log2 of the values' scales
 #pragma unroll
         for (int n = 0; n < NQ; ++n) top[n][0] = top[n][1] = -INFINITY;
 #pragma unroll
-        for (int s = 0; s < SUB; ++s)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {  // keys r, r + 8
-                float k_scale = 1.f;
-                v_log[s][e] = 0.f;
-                if constexpr (E4M3) {
-                    k_scale = ks[s][e];
-                    const float x = lg2(vs[s][e]);
-                    v_log[s][e] = x < 128.f ? x : 0.f;  // a slot that no row sees may hold anything, a NaN too
-                }
-#pragma unroll
-                for (int n = 0; n < NQ; ++n)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float& x = sc[s][n][2 * e + h];
-                        x *= k_scale * scale[n][h];
-                        if (!whole) {
-                            const Seen v = seen_by(a, start + (8 * n + 2 * q4 + h) / G);
-                            if (at[s] < 0 || !v(key0 + 16 * s + 8 * e + r)) x = -INFINITY;
-                        }
-                        top[n][h] = fmaxf(top[n][h], x + v_log[s][e]);
-                    }
+        for (int e = 0; e < 2; ++e) {  // keys r, r + 8
+            float k_scale = 1.f;
+            v_log[e] = 0.f;
+            if constexpr (E4M3) {
+                k_scale = ks[e];
+                const float x = lg2(vs[e]);
+                v_log[e] = x < 128.f ? x : 0.f;  // a slot that no row sees may hold anything, a NaN too
             }
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float& x = sc[n][2 * e + h];
+                    x *= k_scale * scale[n][h];
+                    if (!whole) {
+                        const Seen v = seen_by(a, start + (8 * n + 2 * q4 + h) / G);
+                        if (at < 0 || !v(key0 + 8 * e + r)) x = -INFINITY;
+                    }
+                    top[n][h] = fmaxf(top[n][h], x + v_log[e]);
+                }
+        }
         load_k(at_next);
         bool grown = false;
         auto most_of = [&](int n, int h) {  // this lane's largest score of a row
-            float x = sc[0][n][h];
-#pragma unroll
-            for (int s = 0; s < SUB; ++s) x = fmaxf(x, fmaxf(sc[s][n][h], sc[s][n][2 + h]));
-            return x;
+            return fmaxf(sc[n][h], sc[n][2 + h]);
         };
         auto over_lanes = [&](float x) {  // the largest of a row's eight lanes
 #pragma unroll
@@ -349,32 +308,25 @@ __device__ __forceinline__ void attend_head(const AttendArgs& a, int b, int hk, 
             }
         if (__any_sync(0xffffffffu, grown)) {
             if constexpr (E4M3) {  // once more, without the keys that have no value
-                bool some[SUB][2];
+                uint32_t there[4];
 #pragma unroll
-                for (int s = 0; s < SUB; ++s) {
-                    uint32_t there[4];
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t bits = 0;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t bits = 0;
-#pragma unroll
-                        for (int g = 0; g < VG; ++g)
-                            bits |= vb[s][e][g].x | vb[s][e][g].y | (VB == 16 ? vb[s][e][g].z | vb[s][e][g].w : 0u);
-                        there[e] = __ballot_sync(0xffffffffu, (bits & 0x7f7f7f7fu) != 0);
-                    }
-                    // key r lies with the lanes q4 = r / 2, as the first or second of their four
-                    const uint32_t lanes = 0x11111111u << (r >> 1);
-                    some[s][0] = (there[r & 1 ? 1 : 0] & lanes) != 0, some[s][1] = (there[r & 1 ? 3 : 2] & lanes) != 0;
+                    for (int g = 0; g < VG; ++g) bits |= vb[e][g].x | vb[e][g].y | (VB == 16 ? vb[e][g].z | vb[e][g].w : 0u);
+                    there[e] = __ballot_sync(0xffffffffu, (bits & 0x7f7f7f7fu) != 0);
                 }
+                // key r lies with the lanes q4 = r / 2, as the first or second of their four
+                const uint32_t lanes = 0x11111111u << (r >> 1);
+                const bool some[2] = {((r & 1 ? there[1] : there[0]) & lanes) != 0, ((r & 1 ? there[3] : there[2]) & lanes) != 0};
 #pragma unroll
                 for (int n = 0; n < NQ; ++n)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         float x = -INFINITY;
 #pragma unroll
-                        for (int s = 0; s < SUB; ++s)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e)
-                                if (some[s][e]) x = fmaxf(x, sc[s][n][2 * e + h] + v_log[s][e]);
+                        for (int e = 0; e < 2; ++e)
+                            if (some[e]) x = fmaxf(x, sc[n][2 * e + h] + v_log[e]);
                         top[n][h] = over_lanes(x);
                         const float next = fmaxf(sum_m[n][h], most_of(n, h));
                         l[n][h] *= ex2(sum_m[n][h] - next);
@@ -394,63 +346,59 @@ __device__ __forceinline__ void attend_head(const AttendArgs& a, int b, int hk, 
                         for (int e = 0; e < VE / 2; ++e) o[g][e][n][h] *= keep, o[g][e][n][2 + h] *= keep;
                 }
         }
+        uint32_t w[NQ][2];  // weights as B fragments
 #pragma unroll
-        for (int s = 0; s < SUB; ++s) {
-            uint32_t w[NQ][2];  // weights as B fragments
+        for (int n = 0; n < NQ; ++n)
 #pragma unroll
-            for (int n = 0; n < NQ; ++n)
+            for (int e = 0; e < 2; ++e) {
+                float x[2];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float x[2];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float shift = m[n][h] == -INFINITY ? 0.f : m[n][h];
-                        if constexpr (E4M3) {
-                            x[h] = fminf(ex2(sc[s][n][2 * e + h] + (v_log[s][e] - shift + kTopBits)), kMostWeight);
-                            l[n][h] += ex2(sc[s][n][2 * e + h] - sum_m[n][h]);
-                        } else {
-                            x[h] = ex2(sc[s][n][2 * e + h] - shift);
-                            l[n][h] += x[h];
-                        }
-                    }
+                for (int h = 0; h < 2; ++h) {
+                    const float shift = m[n][h] == -INFINITY ? 0.f : m[n][h];
                     if constexpr (E4M3) {
-                        const __half2 v = __floats2half2_rn(x[0], x[1]);
-                        w[n][e] = transpose8(*reinterpret_cast<const uint32_t*>(&v));
+                        x[h] = fminf(ex2(sc[n][2 * e + h] + (v_log[e] - shift + kTopBits)), kMostWeight);
+                        l[n][h] += ex2(sc[n][2 * e + h] - sum_m[n][h]);
                     } else {
-                        w[n][e] = transpose8(pack_bf16x2(x[0], x[1]));
+                        x[h] = ex2(sc[n][2 * e + h] - shift);
+                        l[n][h] += x[h];
                     }
                 }
+                if constexpr (E4M3) {
+                    const __half2 v = __floats2half2_rn(x[0], x[1]);
+                    w[n][e] = transpose8(*reinterpret_cast<const uint32_t*>(&v));
+                } else {
+                    w[n][e] = transpose8(pack_bf16x2(x[0], x[1]));
+                }
+            }
 #pragma unroll
-            for (int g = 0; g < VG; ++g) {
-                const uint32_t v[4][4] = {{vb[s][0][g].x, vb[s][0][g].y, vb[s][0][g].z, vb[s][0][g].w},
-                                          {vb[s][1][g].x, vb[s][1][g].y, vb[s][1][g].z, vb[s][1][g].w},
-                                          {vb[s][2][g].x, vb[s][2][g].y, vb[s][2][g].z, vb[s][2][g].w},
-                                          {vb[s][3][g].x, vb[s][3][g].y, vb[s][3][g].z, vb[s][3][g].w}};
+        for (int g = 0; g < VG; ++g) {
+            const uint32_t v[4][4] = {{vb[0][g].x, vb[0][g].y, vb[0][g].z, vb[0][g].w},
+                                      {vb[1][g].x, vb[1][g].y, vb[1][g].z, vb[1][g].w},
+                                      {vb[2][g].x, vb[2][g].y, vb[2][g].z, vb[2][g].w},
+                                      {vb[3][g].x, vb[3][g].y, vb[3][g].z, vb[3][g].w}};
 #pragma unroll
-                for (int e = 0; e < VE / 2; ++e) {
-                    uint32_t x[4], f[4];  // values 2 e, 2 e + 1 of the four keys
+            for (int e = 0; e < VE / 2; ++e) {
+                uint32_t x[4], f[4];  // values 2 e, 2 e + 1 of the four keys
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if constexpr (!E4M3)
-                            x[k] = v[k][e];
-                        else
-                            x[k] = e & 1 ? e4m3_to_half2<true>(v[k][e >> 1]) : e4m3_to_half2<false>(v[k][e >> 1]);
-                    }
-                    f[0] = __byte_perm(x[0], x[1], 0x5410), f[1] = __byte_perm(x[0], x[1], 0x7632);
-                    f[2] = __byte_perm(x[2], x[3], 0x5410), f[3] = __byte_perm(x[2], x[3], 0x7632);
+                for (int k = 0; k < 4; ++k) {
+                    if constexpr (!E4M3)
+                        x[k] = v[k][e];
+                    else
+                        x[k] = e & 1 ? e4m3_to_half2<true>(v[k][e >> 1]) : e4m3_to_half2<false>(v[k][e >> 1]);
+                }
+                f[0] = __byte_perm(x[0], x[1], 0x5410), f[1] = __byte_perm(x[0], x[1], 0x7632);
+                f[2] = __byte_perm(x[2], x[3], 0x5410), f[3] = __byte_perm(x[2], x[3], 0x7632);
 #pragma unroll
-                    for (int n = 0; n < NQ; ++n) {
-                        if constexpr (E4M3)
-                            mma_f16(o[g][e][n], f, w[n][0], w[n][1]);
-                        else
-                            mma_bf16(o[g][e][n], f, w[n][0], w[n][1]);
-                    }
+                for (int n = 0; n < NQ; ++n) {
+                    if constexpr (E4M3)
+                        mma_f16(o[g][e][n], f, w[n][0], w[n][1]);
+                    else
+                        mma_bf16(o[g][e][n], f, w[n][0], w[n][1]);
                 }
             }
         }
         load_v(at_next, tiles[i + W] * KEYS);
-#pragma unroll
-        for (int s = 0; s < SUB; ++s) at[s] = at_next[s];
+        at = at_next;
     }
 
     // Join the warps, row by row, in their order
@@ -666,7 +614,7 @@ cudaError_t launch(const AttendArgs& a, int ctas, cudaStream_t st) {
     kernel<<<(unsigned)ctas, F::kWarps * 32, F::kBytes, st>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const long rows = (long)a.c.B * a.c.H * a.c.T;
-    join_kernel<D, F::kKeys><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(a, ctas);
+    join_kernel<D, kBlock><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(a, ctas);
     return cudaGetLastError();
 }
 template <int D, bool E4M3>

@@ -36,11 +36,6 @@ struct Common {
     float tops[16];
 };
 
-__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
-    uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-    return y;
-}
 // A 16 x 16 accumulator (two n-tiles) as the pieces of a B fragment with its rows as k: b[piece][n-tile][half of k].
 __device__ __forceinline__ void to_fragment(const float (&x)[2][4], float s, uint32_t (&b)[2][2][2]) {
 #pragma unroll

@@ -44,15 +44,6 @@ __device__ __forceinline__ void mma_row(float (&acc)[NT][4], const uint32_t (&hi
         }
     }
 }
-// Registers a thread of the four warps of a group, which all take part.
-template <int REGS>
-__device__ __forceinline__ void registers_up() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
-}
-template <int REGS>
-__device__ __forceinline__ void registers_down() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
-}
 
 // Two warps share sixteen rows of a state: each has half of its columns in registers and, within a chunk, half of the
 // tokens. What they tell one another goes through shared memory in the layout of the registers, a lane to the same lane of
