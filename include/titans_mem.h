@@ -344,7 +344,7 @@ typedef struct {
  * T >= 1, T * d < 2^31 and B * H * ceil(T / 64) < 2^30. Up to 24 tokens in fp32 arithmetic, one by one; more in
  * chunks of 64 tokens on the tensor cores, with operands split into fp16 pieces that together hold 22 bits of a
  * value down to 2^-16 of the largest one of its row or chunk (below that, an absolute error of 2^-39 of the largest);
- * for a bf16 y, 11 bits of the state and the writes. An infinity or NaN among a unit's tokens may reach all
+ * for a bf16 y without attn, 11 bits of the state and the writes. An infinity or NaN among a unit's tokens may reach all
  * of its outputs from that token's chunk on, those of the chunk's earlier tokens among them.
  */
 titans_status_t titans_delta_forward(const titans_delta_config *cfg, const void *k, const void *q, const void *v,

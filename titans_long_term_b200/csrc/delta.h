@@ -17,6 +17,9 @@ struct DeltaArgs {
     void* y;
 };
 
+// Pieces of the state, the writes and P that y is taken from (delta_chunks.cu).
+inline int delta_y_pieces(const DeltaArgs& a) { return a.bf16 && !a.attn ? 1 : 2; }
+
 // Token by token, one warp for eight rows of a unit's state (delta_step.cu): any T >= 1.
 cudaError_t launch_delta_tokens(const DeltaArgs& a, cudaStream_t st);
 

@@ -36,16 +36,20 @@ struct Warps {
     static constexpr int kShares = 128 * (kChainRegs + 2 * kOutRegs + kProducerRegs);
 };
 
-template <int D, int RW, typename Tok, bool STATES>
+// YP: pieces of W, E and P that y is taken from. A bf16 y without a gate takes one of each, 11 bits: it is rounded to 8 itself
+// (128 units of 64 chunks, d = 64: 331 us for the call against 388 with two; error against 64 bits 1.69e-3 of y's norm against 1.66e-3,
+// most of it that rounding). A gate's output has its own rounding, beside which sigmoid(y) has to be right to an absolute error
+// that 11 bits of a large state do not give.
+template <int D, int RW, typename Tok, bool STATES, int YP>
 __global__ void __launch_bounds__(Warps<D, RW, sizeof(Tok) == 4 ? 2 : 1, STATES>::kThreads, 1)
     delta_chunks_kernel(DeltaArgs a, const DeltaChunk* recs, int chunks, DeltaStates st) {
     constexpr int NP = sizeof(Tok) == 4 ? 2 : 1;
     using T = Warps<D, RW, NP, STATES>;
     constexpr int kThreads = T::kThreads;
-    using S = Stage<D, RW, NP, NP>;
+    using S = Stage<D, RW, NP, YP>;
     extern __shared__ __align__(1024) unsigned char smem[];
     S* stages = reinterpret_cast<S*>(smem);
-    Exchange<D, NP>* exchanges = reinterpret_cast<Exchange<D, NP>*>(smem + 2 * sizeof(S));
+    Exchange<D, YP>* exchanges = reinterpret_cast<Exchange<D, YP>*>(smem + 2 * sizeof(S));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int kSlices = D / RW;
     const long unit = blockIdx.x / kSlices;
@@ -60,7 +64,7 @@ __global__ void __launch_bounds__(Warps<D, RW, sizeof(Tok) == 4 ? 2 : 1, STATES>
         const Tok* k = static_cast<const Tok*>(a.k) + delta_key_head(a, unit) * a.T * D;
         const Tok* q = static_cast<const Tok*>(a.q) + delta_key_head(a, unit) * a.T * D;
         const Tok* v = static_cast<const Tok*>(a.v) + unit * a.T * D + row_base;
-        Producer<D, RW, Tok, NP, !STATES> next;
+        Producer<D, RW, Tok, YP, !STATES> next;
         auto fetch = [&](int c) { next.fetch(k, q, v, (long)c * kC, (int)min((long)kC, len - (long)c * kC), p); };
         if (used > 0) fetch(0);
         for (int c = 0; c < used; ++c) {
@@ -71,7 +75,7 @@ __global__ void __launch_bounds__(Warps<D, RW, sizeof(Tok) == 4 ? 2 : 1, STATES>
         }
     } else if (T::kPerGroup == 1 && warp < T::kChain) {  // ------------- the state: one warp for sixteen rows
         if constexpr (T::kShift) registers_up<T::kChainRegs>();
-        Exchange<D, NP>& ex = exchanges[warp];
+        Exchange<D, YP>& ex = exchanges[warp];
         const int row = row_base + warp * 16 + (lane >> 2);
         float w[D / 8][4];
         float* W = a.W + unit * D * D + (long)row * D + col2;
@@ -109,6 +113,7 @@ __global__ void __launch_bounds__(Warps<D, RW, sizeof(Tok) == 4 ? 2 : 1, STATES>
                         frag_b<D>(f, ks + e * kC * D * 2, j * 16, kt * 16, lane);
                     });
                     if constexpr (!STATES) ex.w[0][kt][lane] = as_uint4(hi);
+                    if constexpr (!STATES && YP == 2) ex.w[YP - 1][kt][lane] = as_uint4(lo);
                 }
                 if constexpr (!STATES) ex.w_inv[0][lane] = make_float2(i0, i1);
                 i0 *= k_inv, i1 *= k_inv;
@@ -163,6 +168,7 @@ __global__ void __launch_bounds__(Warps<D, RW, sizeof(Tok) == 4 ? 2 : 1, STATES>
                 for (int kt = 0; kt < 4; ++kt) {
                     split_a<8>(x, kt, s0, s1, hi[kt], lo[kt]);
                     ex.e[0][kt][lane] = as_uint4(hi[kt]);
+                    if constexpr (YP == 2) ex.e[YP - 1][kt][lane] = as_uint4(lo[kt]);
                 }
                 ex.e_inv[0][lane] = make_float2(i0, i1);
                 bar_arrive(kOutFull + warp, T::kGroupThreads);
@@ -191,7 +197,7 @@ __global__ void __launch_bounds__(Warps<D, RW, sizeof(Tok) == 4 ? 2 : 1, STATES>
     } else if (warp < T::kChain) {  // ---------------------------------- the state: a pair of warps for sixteen rows
         if constexpr (T::kPerGroup == 2) {
         const int group = warp >> 1, half = warp & 1, tok0 = 32 * half;
-        Exchange<D, NP>& ex = exchanges[group];
+        Exchange<D, YP>& ex = exchanges[group];
         auto pair = [&] { bar_sync(kPair + group, 64); };
         const int row = row_base + group * 16 + (lane >> 2);
         float w[D / 16][4];
@@ -223,7 +229,7 @@ __global__ void __launch_bounds__(Warps<D, RW, sizeof(Tok) == 4 ? 2 : 1, STATES>
                                 [&](int kt, const uint32_t(&hi)[4], const uint32_t(&lo)[4]) {
                                     if constexpr (!STATES) {
                                         ex.w[0][half * (D / 32) + kt][lane] = as_uint4(hi);
-                                        if constexpr (NP == 2) ex.w[NP - 1][half * (D / 32) + kt][lane] = as_uint4(lo);
+                                        if constexpr (YP == 2) ex.w[YP - 1][half * (D / 32) + kt][lane] = as_uint4(lo);
                                     }
                                 });
             if constexpr (!STATES) ex.w_inv[half][lane] = inv;
@@ -302,7 +308,7 @@ __global__ void __launch_bounds__(Warps<D, RW, sizeof(Tok) == 4 ? 2 : 1, STATES>
                     uint32_t hi[4], lo[4];
                     split_a<4>(x, kt, s0, s1, hi, lo);
                     ex.e[0][2 * half + kt][lane] = as_uint4(hi);
-                    if constexpr (NP == 2) ex.e[NP - 1][2 * half + kt][lane] = as_uint4(lo);
+                    if constexpr (YP == 2) ex.e[YP - 1][2 * half + kt][lane] = as_uint4(lo);
                 }
                 ex.e_inv[half][lane] = make_float2(i0, i1);
                 bar_arrive(kOutFull + group, T::kGroupThreads);
@@ -322,7 +328,7 @@ __global__ void __launch_bounds__(Warps<D, RW, sizeof(Tok) == 4 ? 2 : 1, STATES>
     } else if constexpr (!STATES) {  // ---------------------------------- y of sixteen rows, 32 tokens a warp
         if constexpr (T::kShift) registers_down<T::kOutRegs>();
         const int group = (warp - T::kChain) >> 1, half = (warp - T::kChain) & 1, tok0 = 32 * half;
-        const Exchange<D, NP>& ex = exchanges[group];
+        const Exchange<D, YP>& ex = exchanges[group];
         for (int c = 0; c < used; ++c) {
             S& s = stages[c & 1];
             bar_sync(kFull + (c & 1), kThreads);
@@ -333,7 +339,7 @@ __global__ void __launch_bounds__(Warps<D, RW, sizeof(Tok) == 4 ? 2 : 1, STATES>
             float y[4][4] = {}, acc[4][4] = {};
             auto fragments = [&](const uint4(&from)[32], const uint4(&second)[32], uint32_t(&hi)[4], uint32_t(&lo)[4]) {
                 from_uint4(hi, from[lane]);
-                if constexpr (NP == 2) from_uint4(lo, second[lane]);
+                if constexpr (YP == 2) from_uint4(lo, second[lane]);
             };
             auto take = [&](float f0, float f1) {  // y += acc, scaled back
 #pragma unroll
@@ -343,15 +349,15 @@ __global__ void __launch_bounds__(Warps<D, RW, sizeof(Tok) == 4 ? 2 : 1, STATES>
                     acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
                 }
             };
-            // gamma W0 Q^T. bf16: 11 bits of W and E are enough for an output that is rounded to 8.
+            // gamma W0 Q^T
 #pragma unroll
             for (int part = 0; part < kParts; ++part) {
 #pragma unroll
                 for (int i = 0; i < D / 16 / kParts; ++i) {
                     const int kt = part * (D / 16 / kParts) + i;
                     uint32_t hi[4], lo[4];
-                    fragments(ex.w[0][kt], ex.w[NP - 1][kt], hi, lo);
-                    mma_row<NP, NP, 0, 2>(acc, hi, lo, [&](uint32_t(&f)[4], int j, int e) {
+                    fragments(ex.w[0][kt], ex.w[YP - 1][kt], hi, lo);
+                    mma_row<YP, NP, 0, 2>(acc, hi, lo, [&](uint32_t(&f)[4], int j, int e) {
                         frag_b<D>(f, qs + e * kC * D * 2, tok0 + j * 16, kt * 16, lane);
                     });
                 }
@@ -367,14 +373,14 @@ __global__ void __launch_bounds__(Warps<D, RW, sizeof(Tok) == 4 ? 2 : 1, STATES>
             unrolled<4>([&](auto kt) {
                 if (kt < 2 || half) {
                     uint32_t hi[4], lo[4];
-                    fragments(ex.e[0][kt], ex.e[NP - 1][kt], hi, lo);
+                    fragments(ex.e[0][kt], ex.e[YP - 1][kt], hi, lo);
                     auto from = [&](uint32_t(&f)[4], int j, int e) {
                         frag_b<kC>(f, ps + e * kC * kC * 2, tok0 + j * 16, kt * 16, lane);
                     };
                     if (kt == (half ? 3 : 1))
-                        mma_row<NP, NP, 1, 2>(acc, hi, lo, from);
+                        mma_row<YP, YP, 1, 2>(acc, hi, lo, from);
                     else
-                        mma_row<NP, NP, 0, 2>(acc, hi, lo, from);
+                        mma_row<YP, YP, 0, 2>(acc, hi, lo, from);
                 }
                 if (kt == 3 || (kParts == 2 && kt == 1)) {
                     const float2 inv = ex.e_inv[kParts == 2 && kt == 3][lane];
@@ -417,12 +423,12 @@ __global__ void __launch_bounds__(Warps<D, RW, sizeof(Tok) == 4 ? 2 : 1, STATES>
     }
 }
 
-template <int D, int RW, typename Tok, bool STATES>
+template <int D, int RW, typename Tok, bool STATES, int YP>
 cudaError_t launch(const DeltaArgs& a, const void* recs, const DeltaStates& states, cudaStream_t st) {
     constexpr int NP = sizeof(Tok) == 4 ? 2 : 1;
-    constexpr size_t bytes = 2 * sizeof(Stage<D, RW, NP, NP>) + RW / 16 * sizeof(Exchange<D, NP>);
+    constexpr size_t bytes = 2 * sizeof(Stage<D, RW, NP, YP>) + RW / 16 * sizeof(Exchange<D, YP>);
     static_assert(bytes <= 227 * 1024, "two stages and the exchanges fit an SM");
-    auto* kernel = delta_chunks_kernel<D, RW, Tok, STATES>;
+    auto* kernel = delta_chunks_kernel<D, RW, Tok, STATES, YP>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
     using T = Warps<D, RW, NP, STATES>;
@@ -440,17 +446,18 @@ cudaError_t launch(const DeltaArgs& a, const void* recs, const DeltaStates& stat
 
 // Rows of a CTA: as many as shared memory and the barriers have room for, but 32 at d = 128, where 64 would leave most SMs without a
 // CTA at the 32 units of a wide memory's batch.
-template <bool STATES>
+template <bool STATES, int YP>  // YP: in bf16; fp32 has two pieces of everything
 cudaError_t launch(const DeltaArgs& a, const void* recs, const DeltaStates& s, cudaStream_t st) {
     if (a.d == 64)
-        return a.bf16 ? launch<64, 64, __nv_bfloat16, STATES>(a, recs, s, st) : launch<64, 32, float, STATES>(a, recs, s, st);
-    return a.bf16 ? launch<128, 32, __nv_bfloat16, STATES>(a, recs, s, st) : launch<128, 16, float, STATES>(a, recs, s, st);
+        return a.bf16 ? launch<64, 64, __nv_bfloat16, STATES, YP>(a, recs, s, st) : launch<64, 32, float, STATES, 2>(a, recs, s, st);
+    return a.bf16 ? launch<128, 32, __nv_bfloat16, STATES, YP>(a, recs, s, st) : launch<128, 16, float, STATES, 2>(a, recs, s, st);
 }
 
 }  // namespace
 
 cudaError_t launch_delta_chunks(const DeltaArgs& a, const void* chunks, const DeltaStates* states, cudaStream_t st) {
-    return states ? launch<true>(a, chunks, *states, st) : launch<false>(a, chunks, DeltaStates{}, st);
+    if (states) return launch<true, 1>(a, chunks, *states, st);
+    return delta_y_pieces(a) == 2 ? launch<false, 2>(a, chunks, DeltaStates{}, st) : launch<false, 1>(a, chunks, DeltaStates{}, st);
 }
 
 }  // namespace titans

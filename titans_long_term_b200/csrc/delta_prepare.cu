@@ -375,7 +375,7 @@ cudaError_t launch(const DeltaArgs& a, DeltaChunk* out, int chunks, int p_pieces
 cudaError_t launch_delta_prepare(const DeltaArgs& a, void* chunks_out, bool backward, cudaStream_t st) {
     const int chunks = (int)((a.T + kC - 1) / kC);
     DeltaChunk* out = static_cast<DeltaChunk*>(chunks_out);
-    const int n = backward || !a.bf16 ? 2 : 1;  // pieces of P that the other kernels read
+    const int n = backward ? 2 : delta_y_pieces(a);  // pieces of P that the other kernels read
     if (a.d == 64)
         return a.bf16 ? launch<64, __nv_bfloat16>(a, out, chunks, n, st) : launch<64, float>(a, out, chunks, n, st);
     return a.bf16 ? launch<128, __nv_bfloat16>(a, out, chunks, n, st) : launch<128, float>(a, out, chunks, n, st);
