@@ -365,7 +365,8 @@ titans_status_t titans_delta_step(const titans_delta_config *cfg, const void *k,
  * Gradients of <dy, y> + <dW, W_T> for titans_delta_forward without attn, W being the state it starts
  * from (read only) and dW [B, H, d, d] fp32 the adjoint of the state it ends with (NULL = zero):
  *   dk, dq [B, Hk, T, d], summed over the value heads that share them, dv [B, H, T, d];
- *   dg, dbeta [B, H, T] fp32; dW0 [B, H, d, d] fp32.
+ *   dg, dbeta [B, H, T] fp32; dW0 [B, H, d, d] fp32. dg is 0 at a g that forgets all; elsewhere it is a sum over
+ *   the chunk's tokens, off by about 2^-22 of their |q . dq| and |k . dk|, also where exp(g) makes it far smaller.
  * Gradients of the tokens behind `lengths` are zero, and dy is not read there.
  * workspace as in titans_delta_forward, with call = 1. dk, dq, dv in the mode's dtype.
  */

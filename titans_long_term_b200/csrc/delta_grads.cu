@@ -8,7 +8,7 @@
 //   dK  = dKq + dKk
 // A token enters with the factor exp(G_i) where it reads and exp(-G_i) where it writes, so
 //   dG_i = q_i.dQ_i + k_i.dKq_i - k_i.dKk_i,  dG_C += sum_j k_j.(l E A)_j + gamma_C <A, W0>,
-// and dg is the sum of dG from the token to the chunk's end. That needs the products above to fp32's
+// and dg is the sum of dG from the token to the chunk's end (to the next decay of 0, where one comes before that). That needs the products above to fp32's
 // precision also where dk and dq are rounded to bf16: all run on fp16 pieces of 22 bits.
 //
 // One CTA per (key head, chunk) goes through the value heads that share the key head and adds up their dq and dk in
@@ -466,11 +466,23 @@ __global__ void __launch_bounds__(D * 4, D == 64 ? 2 : 1)
                     for (int w = 0; w < kWarps; ++w) x[i] += s.sums[w];
                 }
             }
-            const double sum = warp_prefix(x[0] + x[1], lane);
+            const double sum = warp_prefix(x[0] + x[1], lane), all[2] = {sum - x[1], sum};
+            // Nothing flows through a decay of 0: the sum from such a token on is 0, so it gets none and the tokens before it
+            // take theirs without it
+            bool cut[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int t = kC - 1 - (2 * lane + i);
-                if (t < rows) g.dg[tok + t] = t < n ? (float)(i ? sum : sum - x[1]) : 0.f;
+                cut[i] = s.zeros[t] != (t > 0 ? s.zeros[t - 1] : 0);
+            }
+            const uint32_t later = __ballot_sync(0xffffffffu, cut[0] || cut[1]) & ((1u << lane) - 1);
+            const double nearest = __shfl_sync(0xffffffffu, cut[1] ? all[1] : all[0], later ? 31 - __clz(later) : 0);
+            const double behind = later ? nearest : 0.;
+            const double dg[2] = {cut[0] ? 0. : all[0] - behind, cut[1] ? 0. : all[1] - (cut[0] ? all[0] : behind)};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int t = kC - 1 - (2 * lane + i);
+                if (t < rows) g.dg[tok + t] = t < n ? (float)dg[i] : 0.f;
             }
         }
     }
