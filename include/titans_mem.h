@@ -412,7 +412,8 @@ typedef struct titans_cache *titans_cache_t;
 /* Validates the configuration and allocates the handle and its device status word on the current
  * device, the one that its calls have to be made on. A token whose page is missing (its index is
  * max_pages or more, or its table entry is outside 0..num_pages-1) is skipped by append, read as
- * zeros by read and invisible to attend, and recorded in the status word. */
+ * zeros by read and invisible to attend, and recorded in the status word. The word goes with the handle: destroy it only when
+ * its calls, and graphs that they were captured into, have run for the last time. */
 titans_status_t titans_cache_init(const titans_cache_config *cfg, titans_cache_t *out);
 titans_status_t titans_cache_destroy(titans_cache_t c);
 /* As titans_mem_sync_status, by work on `stream` alone: it waits for no other stream, and what calls on other

@@ -17,7 +17,8 @@ class PagedCache:
     """Keys and values of B sequences in pages, and the attention of new tokens over them. Token p of sequence b
     lies in page table[b, p // page], slot p % page. `dtype` "bf16", or "e4m3": 8 bits with one power-of-two
     scale per token and head, set as the token is written. H query heads share `kv_heads` key/value heads
-    (default H). The tensors are the caller's; the handle belongs to the device that is current here."""
+    (default H). The tensors are the caller's; the handle belongs to the device that is current here, and is kept as
+    long as graphs that its calls were captured into are replayed."""
 
     def __init__(self, d: int, dtype: str, B: int, H: int, kv_heads: Optional[int] = None, page: int = 64,
                  num_pages: int = 0, max_pages: int = 0):

@@ -112,6 +112,7 @@ __device__ __forceinline__ float max64(const uint32_t (&x)[32], const uint32_t (
 // Warps of a CTA in groups of four: NT * kPair of softmax, one group whose first warp issues the MMAs and whose
 // second one brings a bf16 cache, and for an e4m3 cache two that convert it. kPair = 2: two threads share a row, 64
 // keys each, whose chain is half as long; two tiles over an e4m3 cache would have 896 threads of 72 registers then, too few for 64 scores.
+// All forms but one tile over a bf16 cache spill some (84 to 128 bytes a thread stored).
 // Where the launch leaves softmax too few registers it takes over some that the others do not need; what a
 // thread has at launch times the threads covers the new shares (launch() checks it).
 template <bool E4M3, int NT>
@@ -693,8 +694,10 @@ cudaError_t launch(const AttendArgs& a, int splits, cudaStream_t st) {
 // How the rows and keys are shared out: tiles of rows a CTA, and splits of the keys. One CTA fits an SM, and more splits than
 // fill one round of them only add parts to join (128 rows of 16 heads, 8192 keys: 35 us with 148 CTAs at most, 48 us with
 // 296); a split has no less than four tiles of the longest possible sequence, the lengths themselves are on the device.
-// A CTA with two tiles of rows takes 1.45 times as long as one with one (2048 tokens of 16 heads, 8000 keys: 138 us in one
-// round, 191 us in two), so it is the choice where it does not leave too many SMs idle.
+// A CTA with two tiles of rows takes about 1.45 times as long as one with one, so it is the choice where it does not leave too many SMs
+// idle. 2048 tokens of 16 heads on 4, 8000 keys, two tiles in one round against one tile in two: bf16 139 against 192 us at d = 128 and
+// 127 against 164 at d = 64, e4m3 187 against 264 and 156 against 197: factors of 1.42 to 1.59, which choose alike but for
+// batches of two against three rounds.
 struct Shares {
     int tiles, splits;
 };

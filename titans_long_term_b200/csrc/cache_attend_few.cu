@@ -15,14 +15,17 @@
 //                   2 i and 2 i + 1 belong to tile i; the values of two keys are paired by a byte permutation.
 // With keys and values as the 16-row side, eight rows of Q (one token of up to eight heads) cost half the registers and
 // instructions of the other way round. While one block is multiplied the next one's keys and values are on their way, 8 (bf16)
-// or 4 KiB a warp. What bounds it: the instructions of the conversion and the products (e4m3) or the loads in flight (bf16), and the
-// latency of the dependent loads and the join where there is little to read. One token of 16 heads on 4, d = 128, over 8192 keys:
-//   sequences   bf16              e4m3
-//   1           18.5 us           18.5 us
-//   8           34 us             29 us
-//   32          82 us (6.5 TB/s)  68 us (4.0 TB/s)
-// The tile kernel takes 21, 49 and 99 us (bf16) and 25, 55 and 152 us (e4m3). Up to 16 rows this kernel is as fast or faster, except for 16 rows
-// of many bf16 sequences (32: 112 us against 100).
+// or 4 KiB a warp. What bounds it: the loads in flight (three warps a scheduler, most of their stalls waiting for loads; over an
+// e4m3 cache, whose conversion makes a chain of instructions besides, issue slots are 36 % busy and HBM gives 3.5 TB/s), and the latency of the
+// dependent loads and the join where there is little to read. 16 heads on 4, d = 128, 8192 keys in scattered pages, calls in a
+// graph over three caches in turn, this kernel | the tile kernel:
+//   sequences   4 rows, bf16         4 rows, e4m3        16 rows, bf16  16 rows, e4m3
+//   1           17.6 | 20.5 us       16.5 | 24.0 us      19.8 | 20.5    19.8 | 24.6
+//   8           40.3 | 38.2 us       33.4 | 57.0 us      49.7 | 38.0    46.0 | 58.0
+//   32          97 | 106 us          77 | 184 us         130 | 107      115 | 185
+//               (5.5 TB/s)           (3.6 TB/s)
+// So up to 16 rows are its own whatever the type and the batch, which costs a quarter at more than eight rows of several bf16
+// sequences.
 // A page holds at least 16 tokens, so 16 keys need one look into the page table, two blocks ahead of their use.
 //
 // An e4m3 cache is multiplied in fp16, to which one instruction converts two values exactly. Q goes to fp16
@@ -80,8 +83,8 @@ __device__ __forceinline__ int owner(long x, long n, long total) { return (int)(
 // NQ: tiles of eight rows.
 template <int D, bool E4M3, int NQ>
 struct Few {
-    // Loads in flight against registers: with 8 rows 12 warps (32 sequences: 84 us against 91 with 8; e4m3 71 against 85), with 16
-    // rows 8 (114 us against 154 with 12, which spill; e4m3 110 against 107)
+    // Loads in flight against registers: with 8 rows 12 warps (32 sequences: 97 us against 107 with 8; e4m3 77 against 93), with 16
+    // rows 8 (130 us against 173 with 12, which spill; e4m3 115 against 124)
     static constexpr int kWarps = NQ == 2 ? 8 : 12;
     static constexpr int kRows = 8 * NQ;
     static constexpr int kBytes = kWarps * kRows * (D * (int)sizeof(float) + (int)sizeof(float2));

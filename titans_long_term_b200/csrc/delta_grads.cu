@@ -14,7 +14,8 @@
 // One CTA per (key head, chunk) goes through the value heads that share the key head and adds up their dq and dk in
 // registers, in a fixed order. A warp has 32 tokens and 16 columns of dk and dq. Everything a product reads lies in shared memory
 // as fp16 pieces, the two states one after the other and 64 rows at a time; each is read from memory twice, first for
-// its largest value and <A, W0> (W0 kept in registers between the two saves 0.8 %, and spills).
+// its largest value and <A, W0> (W0 kept in registers between the two saves 0.8 % and spills more than the 104 to 260 bytes a
+// thread that the 128 registers leave no room for as it is).
 // 8192 chunks of d = 64: 561 us, 1.5 TB/s of HBM; the L1 data path is 60 % busy and the issue slots 33 %, with the 16 warps that its 109 KB and 128
 // registers a thread leave: phases of loads, products and barriers, of which two CTAs hide one another's.
 #include "delta_common.cuh"
